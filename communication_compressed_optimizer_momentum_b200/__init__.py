@@ -22,10 +22,10 @@ KERNELS = ("worker", "worker_scales", "server", "server_scales", "apply")
 
 
 class OneBitError(RuntimeError):
-    def __init__(self, code: int, where: str):
+    def __init__(self, code: int, where: str, reason: bool = False):
         L = _abi.lib()
         msg = L.onebit_strerror(code).decode()
-        extra = L.onebit_last_error().decode() if code == -4 else ""
+        extra = L.onebit_last_error().decode() if code == -4 or reason else ""
         super().__init__("%s failed: %s (%d)%s" % (where, msg, code, (": " + extra) if extra else ""))
         self.code = code
 
@@ -582,3 +582,8 @@ class ZeroOneAdam(OneBitAdam):
         out = torch.empty(self.d, dtype=torch.float32, device=self.workspace.device)
         onebit01_local_model(self.h, w, x, out, stream)
         return out
+
+
+from .adamw import (  # noqa: E402
+    ADAMW_BLOCK, AdamW, onebit_adamw8_get_state, onebit_adamw8_set_state, onebit_adamw8_step,
+    onebit_adamw_layout, onebit_adamw_step, onebit_grad_norm)

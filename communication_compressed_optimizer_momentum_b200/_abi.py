@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(_PKG, "libonebit_adam.so")
 P = ctypes.c_void_p
 I32, I64, U32P, U64P = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32), \
     ctypes.POINTER(ctypes.c_uint64)
-F32 = ctypes.c_float
+F32, F64, U64 = ctypes.c_float, ctypes.c_double, ctypes.c_uint64
 INT = ctypes.c_int
 
 # name -> (restype, argtypes); mirrors include/onebit_adam.h
@@ -66,6 +66,14 @@ SIGNATURES = {
     "onebit01_dp_init": (INT, [ctypes.POINTER(P), I64, I32, I64, F32, F32, F32, I32, I32, I32,
                                I32]),
     "onebit01_dp_phase": (INT, [P, I32, P, P, F32, P]),
+    "onebit_adamw_layout": (INT, [I32, P, P, ctypes.POINTER(I64)]),
+    "onebit_adamw_step": (INT, [I32, P, P, I32, P, I32, P, P, P, P, P, P, P, F64, F64, F64, F64,
+                                I32, P]),
+    "onebit_adamw8_step": (INT, [I32, P, P, I32, P, I32, P, P, P, P, P, P, U64, P, P, P, F64, F64,
+                                 F64, F64, I32, P]),
+    "onebit_adamw8_get_state": (INT, [I64, P, P, P, P, P, P, I32, P]),
+    "onebit_adamw8_set_state": (INT, [I64, P, P, P, P, P, P, P]),
+    "onebit_grad_norm": (INT, [I32, P, P, I32, F64, I32, P, P]),
     "onebit_strerror": (ctypes.c_char_p, [I32]),
     "onebit_last_error": (ctypes.c_char_p, []),
 }

@@ -1,0 +1,408 @@
+// adamw.cuh -- host side of the AdamW entry points (onebit_adamw_*, onebit_adamw8_*,
+// onebit_grad_norm): argument checks and the launches. Included by onebit_adam.cu, whose error
+// text and helpers it uses.
+#pragma once
+
+#include "kernels_adamw.cuh"
+
+static_assert(sizeof(StepCtl) == ONEBIT_ADAMW_CTL_BYTES, "control block");
+static_assert(sizeof(NormWork) <= ONEBIT_GRAD_NORM_BYTES, "norm work");
+static_assert(kBlk == ONEBIT_ADAMW_BLOCK, "state block");
+
+namespace {
+
+// Table sizes: a short one, so that small calls carry few parameters, and the largest that fits
+// the 32,764 bytes a kernel's parameters may have; longer lists take several launches.
+constexpr int kTabSmall = 64;
+constexpr int kTabLarge = 800;
+constexpr int kSms = 148;
+
+// Half-open address ranges of one call: what it writes must not overlap anything else, or the
+// result would depend on the order in which the blocks run.
+struct Ranges {
+    struct R {
+        uintptr_t lo, hi;
+        bool write;
+    };
+    std::vector<R> r;
+    void add(const void* p, int64_t bytes, bool write) {
+        if (p != nullptr && bytes > 0) {
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+            r.push_back({lo, lo + (uintptr_t)bytes, write});
+        }
+    }
+    bool clash() {
+        const auto by = [](const R& a, const R& b) { return a.lo < b.lo; };
+        if (!std::is_sorted(r.begin(), r.end(), by)) std::sort(r.begin(), r.end(), by);
+        uintptr_t any = 0, written = 0;
+        for (const R& x : r) {
+            if (x.lo < written || (x.write && x.lo < any)) return true;
+            any = std::max(any, x.hi);
+            if (x.write) written = std::max(written, x.hi);
+        }
+        return false;
+    }
+};
+
+int bad(const char* where, const std::string& why, int code = ONEBIT_ERR_ARG) {
+    g_last_error = std::string(where) + ": " + why;
+    return code;
+}
+
+inline bool aligned_to(const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+inline bool known_dtype(int32_t t) { return t == ONEBIT_F32 || t == ONEBIT_BF16; }
+inline int64_t width(int32_t t) { return t == ONEBIT_F32 ? 4 : 2; }
+
+// The tensors of one call, as its kernels take them.
+struct TensorList {
+    int32_t n;
+    const int64_t* numel;
+    void* const* p;          // null: no parameters (grad norm)
+    int32_t ptype;
+    const void* const* g;
+    int32_t gtype;
+    void* const* c;          // null: no copies
+    const double* wd;        // null: no decay
+};
+
+int check_list(const char* where, const TensorList& l, Ranges& ranges, int64_t* blocks) {
+    if (l.n < 0) return bad(where, "negative number of tensors");
+    if (l.n > 0 && (l.numel == nullptr || l.g == nullptr)) return bad(where, "null list");
+    if (!known_dtype(l.gtype) || !known_dtype(l.ptype)) return bad(where, "unknown type");
+    if (l.c != nullptr && l.ptype != ONEBIT_F32)
+        return bad(where, "copies need float32 parameters");
+    int64_t total = 0;
+    for (int32_t i = 0; i < l.n; ++i) {
+        const int64_t n = l.numel[i];
+        if (n < 0 || n > ((int64_t)1 << 39)) return bad(where, "bad size of a tensor");
+        if (n == 0) continue;
+        total += ceil_div(n, kBlk);
+        if (total > ((int64_t)1 << 40)) return bad(where, "too many elements");
+        if (l.g[i] == nullptr || (l.p != nullptr && l.p[i] == nullptr) ||
+            (l.c != nullptr && l.c[i] == nullptr))
+            return bad(where, "null tensor");
+        if (!aligned_to(l.g[i], width(l.gtype)) ||
+            (l.p != nullptr && !aligned_to(l.p[i], width(l.ptype))) ||
+            (l.c != nullptr && !aligned_to(l.c[i], 2)))
+            return bad(where, "tensor not aligned to its elements", ONEBIT_ERR_ALIGN);
+        if (l.wd != nullptr && !(std::isfinite(l.wd[i]) && l.wd[i] >= 0.0))
+            return bad(where, "weight decay must be finite and >= 0");
+    }
+    for (int32_t i = 0; i < l.n; ++i) {
+        ranges.add(l.g[i], l.numel[i] * width(l.gtype), false);
+        if (l.p != nullptr) ranges.add(l.p[i], l.numel[i] * width(l.ptype), true);
+        if (l.c != nullptr) ranges.add(l.c[i], l.numel[i] * 2, true);
+    }
+    *blocks = total;
+    return ONEBIT_OK;
+}
+
+// Tensors from `i` on into one table; returns the next one, the table being full or its block
+// numbers near 32 bits.
+template <int N>
+int32_t fill(const TensorList& l, int32_t i, int64_t blk0, TensorTable<N>& t) {
+    t.n = 0;
+    t.blk0 = blk0;
+    uint64_t b = 0;
+    for (; i < l.n && t.n < N; ++i) {
+        const int64_t n = l.numel[i];
+        if (n == 0) continue;
+        const uint64_t nb = (uint64_t)ceil_div(n, kBlk);
+        if (b + nb > 0x80000000ull) break;
+        const int k = t.n++;
+        t.first[k] = (uint32_t)b;
+        t.g[k] = l.g[i];
+        t.p[k] = l.p != nullptr ? l.p[i] : nullptr;
+        t.c[k] = l.c != nullptr ? l.c[i] : nullptr;
+        t.wd[k] = l.wd != nullptr ? l.wd[i] : 0.0;
+        t.last[k] = (uint16_t)(n - (int64_t)(nb - 1) * kBlk);
+        if (aligned16(t.g[k]) && aligned16(t.p[k]) && aligned16(t.c[k])) t.last[k] |= kTabVec;
+        b += nb;
+    }
+    while (i < l.n && l.numel[i] == 0) ++i;  // empty ones at the end need no launch
+    t.first[t.n] = (uint32_t)b;
+    t.nblk = (uint32_t)b;
+    return i;
+}
+
+unsigned grid_for(uint32_t nblk, int per_sm) {
+    return (unsigned)std::min<int64_t>(std::max<int64_t>(ceil_div(nblk, kWarps), 1),
+                                       kSms * per_sm);
+}
+
+// No C++ exception leaves a C entry point: the lists are the only thing that allocates.
+template <typename F>
+int guarded(F&& f) {
+    try {
+        return f();
+    } catch (...) {
+        return ONEBIT_ERR_SPACE;
+    }
+}
+
+// Queue `launch(table, last)` over the whole list, once at least.
+template <int N, typename F>
+int for_tables(const TensorList& l, F&& launch) {
+    TensorTable<N> t;
+    int32_t i = 0;
+    int64_t blk0 = 0;
+    do {
+        i = fill(l, i, blk0, t);
+        launch(t, i >= l.n);
+        ONEBIT_CUDA(cudaGetLastError());
+        blk0 += t.nblk;
+    } while (i < l.n);
+    return ONEBIT_OK;
+}
+
+template <bool EIGHT, typename PT, typename GT, int N>
+int queue_step(const TensorList& l, StepArgs a, cudaStream_t st) {
+    return for_tables<N>(l, [&](const TensorTable<N>& t, bool last) {
+        a.advance = last ? 1 : 0;
+        if constexpr (EIGHT)
+            k_adamw8<PT, GT, N><<<grid_for(t.nblk, 4), kThreads, 0, st>>>(t, a);
+        else
+            k_adamw<PT, GT, N><<<grid_for(t.nblk, 4), kThreads, 0, st>>>(t, a);
+    });
+}
+
+template <bool EIGHT, int N>
+int queue_step(const TensorList& l, const StepArgs& a, cudaStream_t st) {
+    const bool pf = l.ptype == ONEBIT_F32, gf = l.gtype == ONEBIT_F32;
+    if (pf && gf) return queue_step<EIGHT, float, float, N>(l, a, st);
+    if (pf) return queue_step<EIGHT, float, __nv_bfloat16, N>(l, a, st);
+    if (gf) return queue_step<EIGHT, __nv_bfloat16, float, N>(l, a, st);
+    return queue_step<EIGHT, __nv_bfloat16, __nv_bfloat16, N>(l, a, st);
+}
+
+int check_step(const char* where, StepArgs& a, double eps) {
+    if (!std::isfinite(a.lr)) return bad(where, "lr must be finite");
+    if (!(a.beta1 >= 0.0 && a.beta1 < 1.0) || !(a.beta2 >= 0.0 && a.beta2 < 1.0))
+        return bad(where, "betas must lie in [0, 1)");
+    if (!(std::isfinite(eps) && eps >= 0.0)) return bad(where, "eps must be finite and >= 0");
+    if (a.bias != 0 && a.bias != 1) return bad(where, "bias_correction must be 0 or 1");
+    if (a.ctl == nullptr) return bad(where, "null ctl");
+    if (!aligned_to(a.ctl, 8) || !aligned_to(a.lr_dev, 8) || !aligned_to(a.scale, 4))
+        return bad(where, "ctl, lr_dev or grad_scale not aligned", ONEBIT_ERR_ALIGN);
+    a.eps = (float)eps;
+    a.omb1 = 1.0 - a.beta1;
+    a.omb2 = 1.0 - a.beta2;
+    return ONEBIT_OK;
+}
+
+template <bool EIGHT>
+int adamw_step(const char* where, const TensorList& l, StepArgs a, double eps, void* stream) {
+    int rc = check_step(where, a, eps);
+    if (rc != ONEBIT_OK) return rc;
+    if (l.n > 0 && l.p == nullptr) return bad(where, "null list");
+    Ranges ranges;
+    ranges.r.reserve(3 * (size_t)std::max(l.n, 0) + 8);
+    int64_t blocks = 0;
+    rc = check_list(where, l, ranges, &blocks);
+    if (rc != ONEBIT_OK) return rc;
+    if (blocks > 0) {
+        if (EIGHT) {
+            if (!a.mc || !a.vc || !a.mk || !a.vk) return bad(where, "null state");
+            if (!aligned16(a.mc) || !aligned16(a.vc))
+                return bad(where, "state not 16-byte aligned", ONEBIT_ERR_ALIGN);
+            ranges.add(a.mc, blocks * kBlk, true);
+            ranges.add(a.vc, blocks * kBlk, true);
+            ranges.add(a.mk, blocks, true);
+            ranges.add(a.vk, blocks, true);
+        } else {
+            if (!a.m || !a.v) return bad(where, "null state");
+            if (!aligned16(a.m) || !aligned16(a.v))
+                return bad(where, "state not 16-byte aligned", ONEBIT_ERR_ALIGN);
+            ranges.add(a.m, blocks * kBlk * 4, true);
+            ranges.add(a.v, blocks * kBlk * 4, true);
+        }
+    }
+    ranges.add(a.ctl, sizeof(StepCtl), true);
+    ranges.add(a.scale, 4, false);
+    ranges.add(a.lr_dev, 8, false);
+    if (ranges.clash()) return bad(where, "tensors or states overlap");
+    return l.n <= kTabSmall ? queue_step<EIGHT, kTabSmall>(l, a, as_stream(stream))
+                            : queue_step<EIGHT, kTabLarge>(l, a, as_stream(stream));
+}
+
+StepArgs step_args(void* ctl, const float* grad_scale, const double* lr_dev, double lr,
+                   double beta1, double beta2, int32_t bias) {
+    StepArgs a{};
+    a.lr = lr;
+    a.beta1 = beta1;
+    a.beta2 = beta2;
+    a.lr_dev = lr_dev;
+    a.scale = grad_scale;
+    a.bias = bias;
+    a.ctl = static_cast<StepCtl*>(ctl);
+    return a;
+}
+
+int check_state8(const char* where, int64_t total, const void* mc, const void* vc,
+                 const void* mk, const void* vk, const void* m, const void* v) {
+    if (total < 0 || total % kBlk != 0 || total > ((int64_t)1 << 46))
+        return bad(where, "total must be a multiple of 256");
+    if (total == 0) return ONEBIT_OK;
+    if (m == nullptr && v == nullptr) return bad(where, "neither m nor v");
+    if ((m != nullptr && (mc == nullptr || mk == nullptr)) ||
+        (v != nullptr && (vc == nullptr || vk == nullptr)))
+        return bad(where, "null state");
+    if (!aligned16(mc) || !aligned16(vc) || !aligned16(m) || !aligned16(v))
+        return bad(where, "pointer not 16-byte aligned", ONEBIT_ERR_ALIGN);
+    return ONEBIT_OK;
+}
+
+// The converted vectors and the states they come from or go to: one writes, the other reads.
+bool state8_clash(int64_t total, const void* mc, const void* vc, const void* mk, const void* vk,
+                  const void* m, const void* v, int64_t value_bytes, bool to_state) {
+    Ranges r;
+    if (m != nullptr) {
+        r.add(mc, total, to_state);
+        r.add(mk, total / kBlk, to_state);
+        r.add(m, total * value_bytes, !to_state);
+    }
+    if (v != nullptr) {
+        r.add(vc, total, to_state);
+        r.add(vk, total / kBlk, to_state);
+        r.add(v, total * value_bytes, !to_state);
+    }
+    return r.clash();
+}
+
+template <typename GT, int N>
+int queue_norm(const TensorList& l, NormArgs a, cudaStream_t st) {
+    return for_tables<N>(l, [&](const TensorTable<N>& t, bool) {
+        k_grad_norm<GT, N><<<grid_for(t.nblk, kNormBlocks / kSms), kThreads, 0, st>>>(t, a);
+        a.accumulate = 1;
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+int onebit_adamw_layout(int32_t ntensors, const int64_t* numel, int64_t* offset, int64_t* total) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_adamw_layout";
+        if (ntensors < 0 || total == nullptr || (ntensors > 0 && (numel == nullptr || offset == nullptr)))
+            return bad(where, "bad list");
+        int64_t at = 0;
+        for (int32_t i = 0; i < ntensors; ++i) {
+            if (numel[i] < 0 || numel[i] > ((int64_t)1 << 39)) return bad(where, "bad size of a tensor");
+            offset[i] = at;
+            at += round_up(numel[i], kBlk);
+            if (at > ((int64_t)1 << 48)) return bad(where, "too many elements");
+        }
+        *total = at;
+        return ONEBIT_OK;
+    });
+}
+
+int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* params,
+                      int32_t param_dtype, const void* const* grads, int32_t grad_dtype,
+                      void* const* copies, float* m, float* v, void* ctl,
+                      const double* weight_decay, const float* grad_scale, const double* lr_dev,
+                      double lr, double beta1, double beta2, double eps, int32_t bias_correction,
+                      void* stream) {
+    return guarded([&]() -> int {
+        StepArgs a = step_args(ctl, grad_scale, lr_dev, lr, beta1, beta2, bias_correction);
+        a.m = m;
+        a.v = v;
+        return adamw_step<false>("onebit_adamw_step",
+                                 {ntensors, numel, params, param_dtype, grads, grad_dtype, copies,
+                                  weight_decay},
+                                 a, eps, stream);
+    });
+}
+
+int onebit_adamw8_step(int32_t ntensors, const int64_t* numel, void* const* params,
+                       int32_t param_dtype, const void* const* grads, int32_t grad_dtype,
+                       void* const* copies, uint8_t* m, uint8_t* v, uint8_t* m_exp,
+                       uint8_t* v_exp, void* ctl, uint64_t seed, const double* weight_decay,
+                       const float* grad_scale, const double* lr_dev, double lr, double beta1,
+                       double beta2, double eps, int32_t bias_correction, void* stream) {
+    return guarded([&]() -> int {
+        StepArgs a = step_args(ctl, grad_scale, lr_dev, lr, beta1, beta2, bias_correction);
+        a.mc = m;
+        a.vc = v;
+        a.mk = m_exp;
+        a.vk = v_exp;
+        a.seed = seed;
+        return adamw_step<true>("onebit_adamw8_step",
+                                {ntensors, numel, params, param_dtype, grads, grad_dtype, copies,
+                                 weight_decay},
+                                a, eps, stream);
+    });
+}
+
+int onebit_adamw8_get_state(int64_t total, const uint8_t* m, const uint8_t* v,
+                            const uint8_t* m_exp, const uint8_t* v_exp, void* m_out, void* v_out,
+                            int32_t out_dtype, void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_adamw8_get_state";
+        if (!known_dtype(out_dtype)) return bad(where, "unknown type");
+        const int rc = check_state8(where, total, m, v, m_exp, v_exp, m_out, v_out);
+        if (rc != ONEBIT_OK || total == 0) return rc;
+        if (state8_clash(total, m, v, m_exp, v_exp, m_out, v_out, width(out_dtype), false))
+            return bad(where, "values and states overlap");
+        const int64_t nblk = total / kBlk;
+        const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(nblk, kWarps), kSms * 8);
+        if (out_dtype == ONEBIT_F32)
+            k_adamw8_get<<<grid, kThreads, 0, as_stream(stream)>>>(
+                m, v, m_exp, v_exp, nblk, static_cast<float*>(m_out), static_cast<float*>(v_out));
+        else
+            k_adamw8_get<<<grid, kThreads, 0, as_stream(stream)>>>(
+                m, v, m_exp, v_exp, nblk, static_cast<__nv_bfloat16*>(m_out),
+                static_cast<__nv_bfloat16*>(v_out));
+        ONEBIT_CUDA(cudaGetLastError());
+        return ONEBIT_OK;
+    });
+}
+
+int onebit_adamw8_set_state(int64_t total, uint8_t* m, uint8_t* v, uint8_t* m_exp, uint8_t* v_exp,
+                            const float* m_in, const float* v_in, void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_adamw8_set_state";
+        const int rc = check_state8(where, total, m, v, m_exp, v_exp, m_in, v_in);
+        if (rc != ONEBIT_OK || total == 0) return rc;
+        if (state8_clash(total, m, v, m_exp, v_exp, m_in, v_in, 4, true))
+            return bad(where, "values and states overlap");
+        const int64_t nblk = total / kBlk;
+        const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(nblk, kWarps), kSms * 8);
+        k_adamw8_set<<<grid, kThreads, 0, as_stream(stream)>>>(m, v, m_exp, v_exp, nblk, m_in, v_in);
+        ONEBIT_CUDA(cudaGetLastError());
+        return ONEBIT_OK;
+    });
+}
+
+int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* grads,
+                     int32_t grad_dtype, double max_norm, int32_t accumulate, void* work,
+                     void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_grad_norm";
+        if (!(max_norm > 0.0)) return bad(where, "max_norm must be > 0");
+        if (accumulate != 0 && accumulate != 1) return bad(where, "accumulate must be 0 or 1");
+        if (work == nullptr) return bad(where, "null work");
+        if (!aligned_to(work, 8)) return bad(where, "work not aligned", ONEBIT_ERR_ALIGN);
+        const TensorList l{ntensors, numel, nullptr, ONEBIT_F32, grads, grad_dtype, nullptr, nullptr};
+        Ranges ranges;
+        ranges.r.reserve((size_t)std::max(ntensors, 0) + 1);
+        int64_t blocks = 0;
+        const int rc = check_list(where, l, ranges, &blocks);
+        if (rc != ONEBIT_OK) return rc;
+        ranges.add(work, ONEBIT_GRAD_NORM_BYTES, true);
+        if (ranges.clash()) return bad(where, "work overlaps a gradient");
+        const NormArgs a{max_norm, accumulate, static_cast<NormWork*>(work)};
+        cudaStream_t st = as_stream(stream);
+        const bool small = ntensors <= kTabSmall;
+        if (grad_dtype == ONEBIT_F32)
+            return small ? queue_norm<float, kTabSmall>(l, a, st)
+                         : queue_norm<float, kTabLarge>(l, a, st);
+        return small ? queue_norm<__nv_bfloat16, kTabSmall>(l, a, st)
+                     : queue_norm<__nv_bfloat16, kTabLarge>(l, a, st);
+    });
+}
+
+}  // extern "C"

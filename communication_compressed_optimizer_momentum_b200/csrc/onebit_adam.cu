@@ -1791,3 +1791,8 @@ extern "C" int onebit_compress_static(const float* x, int64_t n, int64_t C, uint
     // so nothing in the shared array has to be cleared first
     return launch_scales(g, part, nch, nseg, kSeg, scales, scales, st);
 }
+
+// ------------------------------------------------------------------------------------------
+// AdamW over a list of tensors
+
+#include "adamw.cuh"

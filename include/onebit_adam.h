@@ -25,6 +25,8 @@
  *     steps and a synchronisation through the same compressed allreduce every H steps, on one
  *     GPU or as data-parallel ranks, with checkpoint/resume;
  *   - onebit_pack, onebit_unpack, onebit_compress_static: one vector's 1-bit message;
+ *   - onebit_adamw_*, onebit_adamw8_*, onebit_grad_norm: AdamW over a list of tensors, with
+ *     states in 32 or in 8 bits, and the global gradient norm that clips its gradients;
  *   - host-only queries: onebit_dp_chunk_range, onebit_server_layout, onebit_strerror,
  *     onebit_last_error.
  *
@@ -552,10 +554,117 @@ int onebit01_dp_init(onebit_adam_t* out, int64_t d, int32_t W, int64_t C, float 
 int onebit01_dp_phase(onebit_adam_t h, int32_t phase, float* x, const void* grads, float lr,
                       void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------------
+ * AdamW over a list of tensors (Loshchilov & Hutter, arXiv 1711.05101: Adam with decoupled weight
+ * decay), the full-precision optimizer of a model whose parameters are many tensors. One step is
+ * one launch over all of them (one more for every 800 tensors). No handle: the caller owns every
+ * buffer, the tensors' addresses are taken anew at every call, and nothing is kept between calls.
+ *
+ *   g = grad_scale * grad ;  m = beta1 m + (1-beta1) g ;  v = beta2 v + (1-beta2) g^2
+ *   p = p (1 - lr wd) - (lr / c1) * m / (sqrt(v) / sqrt(c2) + eps) ;  c_i = 1 - beta_i^t
+ *
+ * in fp32, one IEEE operation each, in the order written; beta1, 1-beta1, lr/c1, 1/sqrt(c2) and
+ * 1 - lr wd are computed in fp64 and rounded once. With bias_correction = 0 (c1 = c2 = 1), wd = 0
+ * and betas that are fp32 values, a step equals onebit_adam_warmup_step with one worker bit for bit.
+ *
+ * Lists: numel, params, grads, copies and weight_decay are host arrays of ntensors entries. A
+ *   tensor is contiguous, aligned to its elements (16-byte alignment is faster), at most 2^39
+ *   elements long, and may be empty (its pointers are then ignored). params and grads are each
+ *   all fp32 or all bf16 (onebit_dtype). copies (or NULL; fp32 params only): bf16 tensors that
+ *   receive the updated parameters rounded to nearest, in the same pass. weight_decay: or NULL (0).
+ * States: one flat vector for m and one for v, in which tensor i begins at offset[i] elements, as
+ *   onebit_adamw_layout gives it: the tensors in order, each rounded up to whole blocks of
+ *   ONEBIT_ADAMW_BLOCK elements. The places behind a tensor belong to no element; they are neither
+ *   read nor written. Zero-filled states are a fresh optimizer's.
+ * ctl: ONEBIT_ADAMW_CTL_BYTES of device memory, 8-byte aligned: int64 steps taken, int64 steps left
+ *   out, double 1 - beta1^t, double 1 - beta2^t, then the library's own. Zero-filled before the
+ *   first step (or the values of step t, to resume). The step counts itself on the device, so a
+ *   step captured into a graph counts every replay. One step at a time may use one ctl.
+ * grad_scale: a device float, or NULL for 1; if it is not finite, the step is left out: parameters
+ *   and states stay as they are and ctl counts it as left out. onebit_grad_norm writes one.
+ * lr_dev: a device double that is read instead of lr, or NULL.
+ *
+ * Refused (ONEBIT_ERR_ARG, ONEBIT_ERR_ALIGN; the reason in onebit_last_error): what the above
+ * excludes; betas outside [0, 1); lr, eps or wd not finite, eps or wd negative; any buffer that is
+ * written and overlaps another of the call (the same parameter twice, a gradient in a parameter's
+ * memory); gradients may share memory.
+ * ------------------------------------------------------------------------------------------
+ */
+#define ONEBIT_ADAMW_BLOCK 256
+#define ONEBIT_ADAMW_CTL_BYTES 64
+#define ONEBIT_GRAD_NORM_BYTES 16384
+
+/* The states' layout for tensors of these lengths: offset[i] of each and the total, in elements
+ * (multiples of ONEBIT_ADAMW_BLOCK). Host only. */
+int onebit_adamw_layout(int32_t ntensors, const int64_t* numel, int64_t* offset, int64_t* total);
+
+/* One step with fp32 states m and v (fp32[total], 16-byte aligned). */
+int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* params,
+                      int32_t param_dtype, const void* const* grads, int32_t grad_dtype,
+                      void* const* copies, float* m, float* v, void* ctl,
+                      const double* weight_decay, const float* grad_scale, const double* lr_dev,
+                      double lr, double beta1, double beta2, double eps, int32_t bias_correction,
+                      void* stream);
+
+/*
+ * The same step with states in 8 bits: m and v are codes (uint8[total], 16-byte aligned), m_exp
+ * and v_exp one exponent k for each block of 256 elements (uint8[total / 256]). A code stands for
+ *   m: (-1)^(c>>7) * f(c & 127, 15) * 2^(k-127) ;   v: f(c, 31) * 2^(k-127)
+ *   f(c, top) = c < 8 ? c/8 * 2^(1-top) : (1 + (c%8)/8) * 2^((c/8) - top)
+ * and k = 255 makes the whole block NaN (it held an infinity, a NaN or a magnitude above
+ * 1.875 * 2^127). The step decodes, computes in fp32 as above, updates the parameters from the
+ * unrounded m and v and encodes them again: k is the smallest with which the block's largest
+ * magnitude does not exceed the largest code, and the rounding is stochastic (up with the
+ * probability of the remainder, in 16 bits), because a change of v by (1-beta2) of itself is far
+ * below the spacing of 8-bit values and would be lost by rounding to nearest. v > 0 never becomes
+ * code 0.
+ * The random bits are a function of seed, the step's number t (from 1) and the element's place i
+ * in the state, so a step is reproducible:
+ *   mix(x): x ^= x>>16, x *= 0x9016D2F5, x ^= x>>15, x *= 0x314549A1, x ^= x>>16   (32 bits)
+ *   key = mix(mix(mix(lo(seed) + G) ^ hi(seed)) + lo(t)) ;  G = 0x9E3779B9
+ *   w = mix(lo(i/8) + key + hi(i/8) * G) ;  x = w + (i%8 + 1) * G
+ *   x ^= x>>15, x *= 0x8A8866C7, x ^= x>>16 ;  16 bits for m: x>>16, for v: x & 0xffff
+ */
+int onebit_adamw8_step(int32_t ntensors, const int64_t* numel, void* const* params,
+                       int32_t param_dtype, const void* const* grads, int32_t grad_dtype,
+                       void* const* copies, uint8_t* m, uint8_t* v, uint8_t* m_exp,
+                       uint8_t* v_exp, void* ctl, uint64_t seed, const double* weight_decay,
+                       const float* grad_scale, const double* lr_dev, double lr, double beta1,
+                       double beta2, double eps, int32_t bias_correction, void* stream);
+
+/*
+ * 8-bit states to values and back, for checkpoints and to go from one state width to the other.
+ * total: a multiple of 256 (onebit_adamw_layout). get: m_out and v_out (fp32 or bf16 by out_dtype,
+ * [total], 16-byte aligned; either may be NULL, both not) receive what the codes stand for, exact
+ * in fp32 and bf16 unless below their range. set: codes and exponents from fp32 values, rounded to
+ * nearest even; values of v below 0 count as 0. Setting what get returned gives the same values.
+ * ONEBIT_ERR_ARG where source and destination overlap.
+ */
+int onebit_adamw8_get_state(int64_t total, const uint8_t* m, const uint8_t* v,
+                            const uint8_t* m_exp, const uint8_t* v_exp, void* m_out, void* v_out,
+                            int32_t out_dtype, void* stream);
+int onebit_adamw8_set_state(int64_t total, uint8_t* m, uint8_t* v, uint8_t* m_exp, uint8_t* v_exp,
+                            const float* m_in, const float* v_in, void* stream);
+
+/*
+ * The l2 norm over all gradients of a list (fp64 sums of squares in a fixed order) and the factor
+ * that clips it: work (device, ONEBIT_GRAD_NORM_BYTES, 8-byte aligned, zero-filled before its first
+ * call) receives double sum of squares, float norm, float scale = min(1, max_norm / norm), or NaN
+ * if the norm is not finite. max_norm > 0, infinity for no clipping. accumulate = 1 adds to the sum
+ * of squares that work holds: several lists of different types (or a sum reduced over ranks) make
+ * one norm. scale's address (work + 12) is a grad_scale of the steps above. One call at a time may
+ * use one work.
+ */
+int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* grads,
+                     int32_t grad_dtype, double max_norm, int32_t accumulate, void* work,
+                     void* stream);
+
 /* Static description of a status code. */
 const char* onebit_strerror(int32_t code);
 
-/* Text of the last CUDA error this thread saw in the library ("" if none). */
+/* Text of the last CUDA error this thread saw in the library, or why one of the entry points that
+ * give a reason last refused its arguments ("" if none). */
 const char* onebit_last_error(void);
 
 #ifdef __cplusplus
