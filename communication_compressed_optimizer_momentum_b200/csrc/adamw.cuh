@@ -118,7 +118,9 @@ int32_t fill(const TensorList& l, int32_t i, int64_t blk0, TensorTable<N>& t) {
         t.c[k] = l.c != nullptr ? l.c[i] : nullptr;
         t.wd[k] = l.wd != nullptr ? l.wd[i] : 0.0;
         t.last[k] = (uint16_t)(n - (int64_t)(nb - 1) * kBlk);
-        if (aligned16(t.g[k]) && aligned16(t.p[k]) && aligned16(t.c[k])) t.last[k] |= kTabVec;
+        if (aligned_to(t.g[k], 8 * width(l.gtype)) && aligned_to(t.p[k], 8 * width(l.ptype)) &&
+            aligned16(t.c[k]))
+            t.last[k] |= kTabVec;
         b += nb;
     }
     while (i < l.n && l.numel[i] == 0) ++i;  // empty ones at the end need no launch
@@ -161,10 +163,12 @@ template <bool EIGHT, typename PT, typename GT, int N>
 int queue_step(const TensorList& l, StepArgs a, cudaStream_t st) {
     return for_tables<N>(l, [&](const TensorTable<N>& t, bool last) {
         a.advance = last ? 1 : 0;
-        if constexpr (EIGHT)
-            k_adamw8<PT, GT, N><<<grid_for(t.nblk, 4), kThreads, 0, st>>>(t, a);
-        else
-            k_adamw<PT, GT, N><<<grid_for(t.nblk, 4), kThreads, 0, st>>>(t, a);
+        if constexpr (EIGHT) {
+            const uint32_t units = (uint32_t)ceil_div(t.nblk + (t.blk0 & (kUnit - 1)), kUnit);
+            k_adamw8<PT, GT, N><<<grid_for(units, kStepBlocks), kThreads, 0, st>>>(t, a);
+        } else {
+            k_adamw<PT, GT, N><<<grid_for(t.nblk, kStepBlocks), kThreads, 0, st>>>(t, a);
+        }
     });
 }
 
@@ -187,6 +191,12 @@ int check_step(const char* where, StepArgs& a, double eps) {
     if (!aligned_to(a.ctl, 8) || !aligned_to(a.lr_dev, 8) || !aligned_to(a.scale, 4))
         return bad(where, "ctl, lr_dev or grad_scale not aligned", ONEBIT_ERR_ALIGN);
     a.eps = (float)eps;
+    a.one = 1.0f;
+    // The fast 8-bit path takes square roots that flush below 2^-126, so a denominator may lose
+    // up to 2^-63 / sqrt(c2), c2 >= 1 - beta2: below 2^-24 of eps if eps is at least this. Above
+    // 2^60 a reciprocal could flush.
+    a.fast = eps * std::sqrt(1.0 - a.beta2) >= 0x1p-39 && eps <= 0x1p60 &&
+             (a.beta1 == 0.0 || a.beta1 >= 0x1p-64) && (a.beta2 == 0.0 || a.beta2 >= 0x1p-64);
     a.omb1 = 1.0 - a.beta1;
     a.omb2 = 1.0 - a.beta2;
     return ONEBIT_OK;
@@ -207,14 +217,16 @@ int adamw_step(const char* where, const TensorList& l, StepArgs a, double eps, v
             if (!a.mc || !a.vc || !a.mk || !a.vk) return bad(where, "null state");
             if (!aligned16(a.mc) || !aligned16(a.vc))
                 return bad(where, "state not 16-byte aligned", ONEBIT_ERR_ALIGN);
+            if (!aligned_to(a.mk, 4) || !aligned_to(a.vk, 4))
+                return bad(where, "exponents not 4-byte aligned", ONEBIT_ERR_ALIGN);
             ranges.add(a.mc, blocks * kBlk, true);
             ranges.add(a.vc, blocks * kBlk, true);
             ranges.add(a.mk, blocks, true);
             ranges.add(a.vk, blocks, true);
         } else {
             if (!a.m || !a.v) return bad(where, "null state");
-            if (!aligned16(a.m) || !aligned16(a.v))
-                return bad(where, "state not 16-byte aligned", ONEBIT_ERR_ALIGN);
+            if (!aligned_to(a.m, 32) || !aligned_to(a.v, 32))
+                return bad(where, "state not 32-byte aligned", ONEBIT_ERR_ALIGN);
             ranges.add(a.m, blocks * kBlk * 4, true);
             ranges.add(a.v, blocks * kBlk * 4, true);
         }
@@ -241,7 +253,8 @@ StepArgs step_args(void* ctl, const float* grad_scale, const double* lr_dev, dou
 }
 
 int check_state8(const char* where, int64_t total, const void* mc, const void* vc,
-                 const void* mk, const void* vk, const void* m, const void* v) {
+                 const void* mk, const void* vk, const void* m, const void* v,
+                 int64_t value_bytes) {
     if (total < 0 || total % kBlk != 0 || total > ((int64_t)1 << 46))
         return bad(where, "total must be a multiple of 256");
     if (total == 0) return ONEBIT_OK;
@@ -249,8 +262,12 @@ int check_state8(const char* where, int64_t total, const void* mc, const void* v
     if ((m != nullptr && (mc == nullptr || mk == nullptr)) ||
         (v != nullptr && (vc == nullptr || vk == nullptr)))
         return bad(where, "null state");
-    if (!aligned16(mc) || !aligned16(vc) || !aligned16(m) || !aligned16(v))
-        return bad(where, "pointer not 16-byte aligned", ONEBIT_ERR_ALIGN);
+    if (!aligned16(mc) || !aligned16(vc))
+        return bad(where, "state not 16-byte aligned", ONEBIT_ERR_ALIGN);
+    if (!aligned_to(mk, 4) || !aligned_to(vk, 4))
+        return bad(where, "exponents not 4-byte aligned", ONEBIT_ERR_ALIGN);
+    if (!aligned_to(m, 8 * value_bytes) || !aligned_to(v, 8 * value_bytes))
+        return bad(where, "values not aligned to eight of them", ONEBIT_ERR_ALIGN);
     return ONEBIT_OK;
 }
 
@@ -343,7 +360,7 @@ int onebit_adamw8_get_state(int64_t total, const uint8_t* m, const uint8_t* v,
     return guarded([&]() -> int {
         const char* where = "onebit_adamw8_get_state";
         if (!known_dtype(out_dtype)) return bad(where, "unknown type");
-        const int rc = check_state8(where, total, m, v, m_exp, v_exp, m_out, v_out);
+        const int rc = check_state8(where, total, m, v, m_exp, v_exp, m_out, v_out, width(out_dtype));
         if (rc != ONEBIT_OK || total == 0) return rc;
         if (state8_clash(total, m, v, m_exp, v_exp, m_out, v_out, width(out_dtype), false))
             return bad(where, "values and states overlap");
@@ -365,7 +382,7 @@ int onebit_adamw8_set_state(int64_t total, uint8_t* m, uint8_t* v, uint8_t* m_ex
                             const float* m_in, const float* v_in, void* stream) {
     return guarded([&]() -> int {
         const char* where = "onebit_adamw8_set_state";
-        const int rc = check_state8(where, total, m, v, m_exp, v_exp, m_in, v_in);
+        const int rc = check_state8(where, total, m, v, m_exp, v_exp, m_in, v_in, 4);
         if (rc != ONEBIT_OK || total == 0) return rc;
         if (state8_clash(total, m, v, m_exp, v_exp, m_in, v_in, 4, true))
             return bad(where, "values and states overlap");

@@ -569,7 +569,7 @@ int onebit01_dp_phase(onebit_adam_t h, int32_t phase, float* x, const void* grad
  * and betas that are fp32 values, a step equals onebit_adam_warmup_step with one worker bit for bit.
  *
  * Lists: numel, params, grads, copies and weight_decay are host arrays of ntensors entries. A
- *   tensor is contiguous, aligned to its elements (16-byte alignment is faster), at most 2^39
+ *   tensor is contiguous, aligned to its elements (to eight of them is faster), at most 2^39
  *   elements long, and may be empty (its pointers are then ignored). params and grads are each
  *   all fp32 or all bf16 (onebit_dtype). copies (or NULL; fp32 params only): bf16 tensors that
  *   receive the updated parameters rounded to nearest, in the same pass. weight_decay: or NULL (0).
@@ -599,7 +599,7 @@ int onebit01_dp_phase(onebit_adam_t h, int32_t phase, float* x, const void* grad
  * (multiples of ONEBIT_ADAMW_BLOCK). Host only. */
 int onebit_adamw_layout(int32_t ntensors, const int64_t* numel, int64_t* offset, int64_t* total);
 
-/* One step with fp32 states m and v (fp32[total], 16-byte aligned). */
+/* One step with fp32 states m and v (fp32[total], 32-byte aligned). */
 int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* params,
                       int32_t param_dtype, const void* const* grads, int32_t grad_dtype,
                       void* const* copies, float* m, float* v, void* ctl,
@@ -609,7 +609,7 @@ int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* param
 
 /*
  * The same step with states in 8 bits: m and v are codes (uint8[total], 16-byte aligned), m_exp
- * and v_exp one exponent k for each block of 256 elements (uint8[total / 256]). A code stands for
+ * and v_exp one exponent k for each block of 256 elements (uint8[total / 256], 4-byte aligned). A code stands for
  *   m: (-1)^(c>>7) * f(c & 127, 15) * 2^(k-127) ;   v: f(c, 31) * 2^(k-127)
  *   f(c, top) = c < 8 ? c/8 * 2^(1-top) : (1 + (c%8)/8) * 2^((c/8) - top)
  * and k = 255 makes the whole block NaN (it held an infinity, a NaN or a magnitude above
@@ -618,7 +618,9 @@ int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* param
  * magnitude does not exceed the largest code, and the rounding is stochastic (up with the
  * probability of the remainder, in 16 bits), because a change of v by (1-beta2) of itself is far
  * below the spacing of 8-bit values and would be lost by rounding to nearest. v > 0 never becomes
- * code 0.
+ * code 0. Where eps >= 2^-39 / sqrt(1 - beta2), which holds for every usual eps, the quotient
+ * m / (...) comes from the hardware's approximate square root and reciprocal and a fused
+ * multiply-add: within 2^-21 of itself, below the rounding of p; codes and exponents are exact.
  * The random bits are a function of seed, the step's number t (from 1) and the element's place i
  * in the state, so a step is reproducible:
  *   mix(x): x ^= x>>16, x *= 0x9016D2F5, x ^= x>>15, x *= 0x314549A1, x ^= x>>16   (32 bits)
@@ -636,7 +638,7 @@ int onebit_adamw8_step(int32_t ntensors, const int64_t* numel, void* const* para
 /*
  * 8-bit states to values and back, for checkpoints and to go from one state width to the other.
  * total: a multiple of 256 (onebit_adamw_layout). get: m_out and v_out (fp32 or bf16 by out_dtype,
- * [total], 16-byte aligned; either may be NULL, both not) receive what the codes stand for, exact
+ * [total], aligned to 8 values; either may be NULL, both not) receive what the codes stand for, exact
  * in fp32 and bf16 unless below their range. set: codes and exponents from fp32 values, rounded to
  * nearest even; values of v below 0 count as 0. Setting what get returned gives the same values.
  * ONEBIT_ERR_ARG where source and destination overlap.

@@ -121,10 +121,18 @@ def test_step_refusals(lib, eight, change, code, why):
     assert (rc, why in text) == (code, True), (rc, text)
 
 
+def test_states_alignment(lib):
+    """fp32 states are read 32 bytes at a time, exponents four at a time, codes 16-byte aligned."""
+    assert call_step(lib, False, m=AT["m"] + 16)[0] == -2
+    assert call_step(lib, False, v=AT["v"] + 16)[0] == -2
+    assert call_step(lib, True, me=AT["me"] + 2)[0] == -2
+    assert call_step(lib, True, ve=AT["ve"] + 1)[0] == -2
+
+
 def test_step8_refuses_missing_or_overlapping_exponents(lib):
     assert call_step(lib, True, me=None)[0] == -1
     assert call_step(lib, True, ve=None)[0] == -1
-    rc, text = call_step(lib, True, ve=AT["me"] + 5)          # 4 + 2 blocks: 6 exponents
+    rc, text = call_step(lib, True, ve=AT["me"] + 4)          # 4 + 2 blocks: 6 exponents
     assert rc == -1 and "overlap" in text
     rc, text = call_step(lib, True, me=AT["m"])
     assert rc == -1 and "overlap" in text
@@ -155,6 +163,7 @@ def test_norm_refusals(lib, change, code, why):
 @pytest.mark.parametrize("change,code", [
     (dict(total=-256), -1), (dict(total=100), -1), (dict(a=None, b=None), -1),
     (dict(mc=None), -1), (dict(vk=None), -1), (dict(mc=0x1008), -2), (dict(a=0x50008), -2),
+    (dict(b=0x60010), -2), (dict(mk=0x3002), -2),
     (dict(b=0x50100), -1),                                    # the two values overlap
     (dict(a=0x1100), -1),                                     # a value in the codes
 ], ids=lambda x: None)

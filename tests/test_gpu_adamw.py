@@ -320,6 +320,25 @@ def test_sizes_of_gradients(size, eight):
     check_step(pr, None, 2)
 
 
+@pytest.mark.parametrize("align", [1, 16])
+def test_8_bit_states_at_every_power_of_two(align):
+    """One tensor of whole and one of odd length for each size of gradients from 2^-70 to 2^50, so
+    that the blocks' exponents pass every border of the kernel's fast form, from fresh states on;
+    some blocks hold a single value."""
+    powers = list(range(-70, 51))
+    sizes = [n for _ in powers for n in (1024, 300)]
+    pr = Problem(sizes, torch.float32, torch.float32, align, seed=21, eight=True)
+    gen = torch.Generator(DEV).manual_seed(5)
+    for x in pr.state:
+        x.zero_()
+    pr.inside[:] = True
+    for t in (1, 2, 3):
+        for i, g in enumerate(pr.g):
+            g.copy_(torch.randn(g.shape, device=DEV, generator=gen) * 2.0 ** powers[i // 2])
+            g[256:511] = 0.0
+        check_step(pr, None, t)
+
+
 def test_v_above_zero_never_reads_as_zero():
     """A block with one large and many tiny gradients: v of the tiny ones stays above 0, so that no
     later denominator is eps alone, and exact zeros stay 0."""
