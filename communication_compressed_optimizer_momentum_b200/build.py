@@ -1,5 +1,6 @@
 """Build step for the CUDA library: compiles ``csrc/onebit_adam.cu`` for sm_100a into
-``libonebit_adam.so`` next to this file (in-tree, so the built library travels with the repo).
+``libonebit_adam.so`` next to this file (in-tree, so the built library travels with the repo), and
+``csrc/binding.cpp``, the binding's native part for lists of tensors, into ``_binding.so``.
 
 Run ``python -m communication_compressed_optimizer_momentum_b200.build`` or call ``build()``.
 """
@@ -30,6 +31,10 @@ NVCC_FLAGS = [
 ]
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = os.path.join(SRC_DIR, "binding.cpp")
+
+
 def nvcc() -> str:
     cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
@@ -43,7 +48,9 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if it is missing or older than its sources; return its path."""
+    """Compile the library (and the binding's native part) if it is missing or older than its
+    sources; return the library's path."""
+    build_binding(force)
     if not force and not stale():
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()
@@ -54,6 +61,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the binding's native part if it is missing or older than its sources."""
+    deps = (BINDING_SOURCE, os.path.join(INCLUDE, "onebit_adam.h"))
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(BINDING) >= os.path.getmtime(p) for p in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    includes = [INCLUDE, os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+         "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+         *["-I" + p for p in includes], "-o", tmp, BINDING_SOURCE, "-L" + lib,
+         "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
