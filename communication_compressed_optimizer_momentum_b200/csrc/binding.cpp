@@ -82,46 +82,50 @@ const at::Tensor& vector(const py::handle& o, at::ScalarType type, int64_t numel
     return t;
 }
 
-// A list of tensors of one type on one device.
+// A list of tensors of one type on one device. The tensors are the Python objects' own: the list
+// (kept alive here) holds them, and the GIL is not given up before the call is over.
 struct List {
-    std::vector<at::Tensor> tensors;
+    py::object seq;
+    std::vector<const at::Tensor*> tensors;
     std::vector<int64_t> numel;
     std::vector<void*> data;
     at::ScalarType type = at::kFloat;
     int32_t n() const { return (int32_t)tensors.size(); }
 };
 
-List list_of(const py::handle& o, const std::string& name, const c10::Device* device,
+List list_of(const py::handle& o, const char* name, const c10::Device* device,
              const std::vector<int64_t>* numel) {
-    const py::object seq = py::reinterpret_steal<py::object>(
-        PySequence_Fast(o.ptr(), (name + " must be a list of tensors").c_str()));
-    if (!seq) throw py::error_already_set();
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq.ptr());
-    if (n > INT32_MAX) throw py::value_error(name + ": too many tensors");
     List l;
-    l.tensors.reserve(n);
-    l.numel.reserve(n);
-    l.data.reserve(n);
+    l.seq = py::reinterpret_steal<py::object>(
+        PySequence_Fast(o.ptr(), (std::string(name) + " must be a list of tensors").c_str()));
+    if (!l.seq) throw py::error_already_set();
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(l.seq.ptr());
+    if (n > INT32_MAX) throw py::value_error(std::string(name) + ": too many tensors");
+    l.tensors.resize(n);
+    l.numel.resize(n);
+    l.data.resize(n);
+    c10::Device first(c10::kCPU);
     for (Py_ssize_t i = 0; i < n; ++i) {
-        PyObject* p = PySequence_Fast_GET_ITEM(seq.ptr(), i);
-        if (!THPVariable_Check(p)) throw py::type_error(name + " must be a list of tensors");
+        PyObject* p = PySequence_Fast_GET_ITEM(l.seq.ptr(), i);
+        if (!THPVariable_Check(p))
+            throw py::type_error(std::string(name) + " must be a list of tensors");
         const at::Tensor& t = THPVariable_Unpack(p);
         if (i == 0) {
             check_cuda(t, name, device);
             l.type = t.scalar_type();
-        } else if (t.scalar_type() != l.type || t.device() != l.tensors[0].device()) {
-            throw py::value_error(name + " must be of one type on one device, got " +
-                                  type_name(l.type) + " on " + l.tensors[0].device().str() +
-                                  " and " + type_name(t.scalar_type()) + " on " +
-                                  t.device().str());
+            first = t.device();
+        } else if (t.scalar_type() != l.type || t.device() != first) {
+            throw py::value_error(std::string(name) + " must be of one type on one device, got " +
+                                  type_name(l.type) + " on " + first.str() + " and " +
+                                  type_name(t.scalar_type()) + " on " + t.device().str());
         }
-        if (!t.is_contiguous()) throw py::value_error(name + " must be contiguous");
-        l.tensors.push_back(t);
-        l.numel.push_back(t.numel());
-        l.data.push_back(t.data_ptr());
+        if (!t.is_contiguous()) throw py::value_error(std::string(name) + " must be contiguous");
+        l.tensors[i] = &t;
+        l.numel[i] = t.numel();
+        l.data[i] = t.data_ptr();
     }
     if (numel != nullptr && l.numel != *numel)
-        throw py::value_error(name + " have lengths other than the parameters'");
+        throw py::value_error(std::string(name) + " have lengths other than the parameters'");
     return l;
 }
 
@@ -154,9 +158,9 @@ class Queue {
         if (stream_.stream() != current_.stream() && t.defined() && t.numel() > 0)
             t.record_stream(stream_.unwrap());
     }
-    void uses(const std::vector<at::Tensor>& ts) const {
+    void uses(const std::vector<const at::Tensor*>& ts) const {
         if (stream_.stream() == current_.stream()) return;
-        for (const at::Tensor& t : ts) uses(t);
+        for (const at::Tensor* t : ts) uses(*t);
     }
 
   private:
@@ -212,7 +216,13 @@ void step(const char* where, const py::object& params, const py::object& grads,
     if (PyFloat_Check(decay.ptr()) || PyLong_Check(decay.ptr())) {
         wd.assign(p.n(), py::cast<double>(decay));
     } else {
-        wd = py::cast<std::vector<double>>(decay);
+        const py::object seq = py::reinterpret_steal<py::object>(
+            PySequence_Fast(decay.ptr(), "weight_decay must be a number or a list of numbers"));
+        if (!seq) throw py::error_already_set();
+        wd.resize(PySequence_Fast_GET_SIZE(seq.ptr()));
+        for (size_t i = 0; i < wd.size(); ++i)
+            wd[i] = PyFloat_AsDouble(PySequence_Fast_GET_ITEM(seq.ptr(), i));
+        if (PyErr_Occurred()) throw py::error_already_set();
         if ((int64_t)wd.size() != p.n())
             throw py::value_error(std::to_string(wd.size()) + " weight decays for " +
                                   std::to_string(np) + " parameters");
@@ -326,12 +336,12 @@ py::tuple grad_norm(const py::object& grads, double max_norm, const py::object& 
     if (!work.defined() && g.n() == 0)
         throw py::value_error("no gradients and no work to say where");
     const int32_t code = dtype_code(g.type, "grads");
-    const c10::Device device = work.defined() ? expected : g.tensors[0].device();
+    const c10::Device device = work.defined() ? expected : g.tensors[0]->device();
     const Queue q(device, stream);
     if (!work.defined()) {
         const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(
             reinterpret_cast<cudaStream_t>(q.handle()), device.index()));
-        work = at::zeros({ONEBIT_GRAD_NORM_BYTES}, g.tensors[0].options().dtype(at::kByte));
+        work = at::zeros({ONEBIT_GRAD_NORM_BYTES}, g.tensors[0]->options().dtype(at::kByte));
     }
     refuse(p_norm(g.n(), g.numel.data(), g.data.data(), code, max_norm, accumulate ? 1 : 0,
                   work.data_ptr(), q.handle()),
