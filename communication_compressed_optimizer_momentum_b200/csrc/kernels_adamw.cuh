@@ -201,13 +201,14 @@ __device__ __forceinline__ float keep_of(const StepArgs& a, double wd) {
     return (float)__dsub_rn(1.0, __dmul_rn(step_lr(a), wd));
 }
 
-// Count the step once every block of its last launch is done with the scalars.
+// Count the step once every block of its last launch is done. Only reads of ctl have to come
+// before this, and every thread has used what it read by the barrier: no fence (which small calls
+// feel: 240 tensors of 1 to 4 thousand elements, 6.4 us with one).
 __device__ __forceinline__ void step_done(const StepArgs& a, bool skip) {
     if (!a.advance) return;
     __syncthreads();
     if (threadIdx.x != 0) return;
     StepCtl* c = a.ctl;
-    __threadfence();
     if (atomicAdd(&c->ticket, 1u) != gridDim.x - 1) return;
     c->ticket = 0;
     if (skip) {
