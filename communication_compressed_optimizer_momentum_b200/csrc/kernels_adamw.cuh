@@ -138,6 +138,12 @@ __device__ __forceinline__ void store(T* p, int lane, int len, const float (&o)[
 // ------------------------------------------------------------------------------------------
 // the walk over the tensors
 
+// This warp within its thread block, in a form that lets the compiler keep what follows from it
+// in uniform registers (8-bit step, fp32 and bf16: 787 -> 729 us, all bf16 648 -> 623).
+__device__ __forceinline__ uint32_t warp_of_block() {
+    return __shfl_sync(kFull, threadIdx.x >> 5, 0);
+}
+
 // The tensor that block b belongs to.
 template <int N>
 __device__ __forceinline__ int tensor_of(const TensorTable<N>& t, uint32_t b) {
@@ -613,16 +619,18 @@ __device__ __forceinline__ bool adamw8_fast(const Block8<PT, GT>& in, const Step
             yv[i + j] = (__float_as_uint(zv[j]) << 4) + (hi ^ lo);
         }
     }
-    const uint32_t least = min(min(min(yv[0], yv[1]), min(yv[2], yv[3])),
-                               min(min(yv[4], yv[5]), min(yv[6], yv[7])));
-    if (least < 1u << 24) {
+    uint32_t c0 = top_bytes(yv[0], yv[1], yv[2], yv[3]), c1 = top_bytes(yv[4], yv[5], yv[6], yv[7]);
+    // where a word has a zero byte: codes of 0 that stand for positive values become 1
+    if ((((c0 - 0x01010101u) & ~c0) | ((c1 - 0x01010101u) & ~c1)) & 0x80808080u) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (vv[i] > 0.0f) yv[i] = max(yv[i], 1u << 24);
+        c0 = top_bytes(yv[0], yv[1], yv[2], yv[3]);
+        c1 = top_bytes(yv[4], yv[5], yv[6], yv[7]);
     }
     out.codes(
         make_uint2(top_bytes(ym[0], ym[1], ym[2], ym[3]), top_bytes(ym[4], ym[5], ym[6], ym[7])),
-        make_uint2(top_bytes(yv[0], yv[1], yv[2], yv[3]), top_bytes(yv[4], yv[5], yv[6], yv[7])));
+        make_uint2(c0, c1));
     return true;
 }
 
@@ -733,7 +741,7 @@ k_adamw8(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
         const uint32_t key = step_key(a.seed, a.ctl->t + 1);
         const uint32_t lead = (uint32_t)t.blk0 & (kUnit - 1);
         const uint32_t units = units_of(t, lead);
-        uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+        uint32_t u = blockIdx.x * kWarps + warp_of_block();
         int i = first_tensor(t, lead, u), known = -1;
         float keep = 0.0f;
         for (; u < units; u += gridDim.x * kWarps) {
@@ -768,8 +776,8 @@ k_adamw8(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
                     if (!adamw8_fast(in[q % 2], s, a, keep, kh, (uint32_t)G + q * 32, km, kv, out))
                         left |= 1u << q;
                     // the new exponent goes in at the top as the old one leaves below
-                    mk = mk >> 8 | km << 24;
-                    vk = vk >> 8 | kv << 24;
+                    mk = __byte_perm(mk, km, 0x4321);
+                    vk = __byte_perm(vk, kv, 0x4321);
                     const int l = q + 2;
                     if (l < kUnit)
                         in[l % 2].load(p + l * kBlk, g + l * kBlk, mc + l * kBlk, vc + l * kBlk,
