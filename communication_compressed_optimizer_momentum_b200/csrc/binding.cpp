@@ -168,6 +168,12 @@ class Queue {
     c10::cuda::CUDAStream current_, stream_;
 };
 
+// Autograd takes note of the change.
+void changed(const std::vector<const at::Tensor*>& ts) {
+    for (const at::Tensor* t : ts)
+        if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 int64_t blocks_of(const std::vector<int64_t>& numel) {
     int64_t b = 0;
     for (const int64_t n : numel) b += (n + ONEBIT_ADAMW_BLOCK - 1) / ONEBIT_ADAMW_BLOCK;
@@ -250,6 +256,8 @@ void step(const char* where, const py::object& params, const py::object& grads,
                        st[0]->data_ptr<float>(), st[1]->data_ptr<float>(), ctl.data_ptr(),
                        wd.data(), scale_p, lr_p, lr, beta1, beta2, eps, bias ? 1 : 0, q.handle());
     refuse(rc, where);
+    changed(p.tensors);
+    changed(c.tensors);
     q.uses(p.tensors);
     q.uses(g.tensors);
     q.uses(c.tensors);

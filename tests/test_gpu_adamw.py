@@ -35,6 +35,7 @@ class Problem:
         rng = np.random.default_rng(seed)
         self.sizes = sizes
         self.eight = eight
+        self.hp = dict(HP)
         self.offsets, self.total = ob.onebit_adamw_layout(sizes)
         self.at = []
         n = 3 if align == 1 else 0                    # odd addresses, not only odd distances
@@ -93,7 +94,7 @@ class Problem:
     def step(self, lr=None, scale=None, seed=5, bias=True, stream=None, grads=None):
         lr = HP["lr"] if lr is None else lr
         kw = dict(copies=self.c, grad_scale=scale, bias_correction=bias, stream=stream)
-        args = (self.ctl, lr, HP["beta1"], HP["beta2"], HP["eps"], self.wd)
+        args = (self.ctl, lr, self.hp["beta1"], self.hp["beta2"], self.hp["eps"], self.wd)
         grads = self.g if grads is None else grads
         if self.eight:
             ob.onebit_adamw8_step(self.p, grads, *self.state, *args, seed=seed, **kw)
@@ -117,7 +118,7 @@ def check_step(pr, scale, t, seed=5, bias=True):
     before = [x.cpu().numpy().copy() for x in pr.state]
     s = None if scale is None else torch.tensor([scale], dtype=torch.float32, device=DEV)
     s64 = 1.0 if scale is None else float(np.float32(scale))
-    pr.set_t(t - 1)
+    pr.set_t(t - 1, pr.hp["beta1"], pr.hp["beta2"])
     pr.step(scale=s, seed=seed, bias=bias)
     torch.cuda.synchronize()
     assert pr.ctl[:2].tolist() == [t, 0]
@@ -138,7 +139,7 @@ def check_step(pr, scale, t, seed=5, bias=True):
             continue
         o = slice(pr.offsets[i], pr.offsets[i] + n)
         (p1, m1, v1), (ep, em, ev) = ref.step64(
-            p0[i], g0[i], m0[o], v0[o], t, HP["lr"], HP["beta1"], HP["beta2"], HP["eps"],
+            p0[i], g0[i], m0[o], v0[o], t, HP["lr"], pr.hp["beta1"], pr.hp["beta2"], pr.hp["eps"],
             pr.wd[i], s64, bias)
         got = host(pr.p[i])
         bound = ep if ptype == torch.float32 else ref.bf16_bound(p1, ep)
@@ -150,7 +151,7 @@ def check_step(pr, scale, t, seed=5, bias=True):
             assert (np.abs(after[1][o] - v1) <= ev).all(), (i, n)
             continue
         # 8 bits: the exact code that the documented rounding of the fp32 moments gives
-        m32, v32 = ref.moments32(g0[i], m0[o], v0[o], HP["beta1"], HP["beta2"], s64)
+        m32, v32 = ref.moments32(g0[i], m0[o], v0[o], pr.hp["beta1"], pr.hp["beta2"], s64)
         blocks = -(-n // BLOCK)
         words = ref.random_words(np.arange(o.start, o.start + blocks * BLOCK), seed, t)
         for x, x64, e64, codes, exps, signed, r in (
@@ -212,6 +213,19 @@ def test_address_does_not_matter(eight):
         a.step()
         b.step()
     assert same_bits(a.state + a.p + a.c + [a.ctl[:4]], b.state + b.p + b.c + [b.ctl[:4]])
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
+@pytest.mark.parametrize("beta1,beta2,eps", [
+    (0.0, 0.999, 1e-8), (0.9, 0.0, 1e-8), (0.0, 0.0, 1e-3), (0.95, 0.9999, 1e-6),
+    (0.9, 0.999, 1e-14), (1e-30, 0.999, 1e-8), (0.9, 0.999, 1e25)])
+def test_other_hyperparameters(beta1, beta2, eps, eight):
+    """Betas of 0 and next to it, and an eps that is too small or too large for the 8-bit step's
+    approximations: the plain form."""
+    pr = Problem(SHORT, torch.float32, torch.bfloat16, 16, seed=12, eight=eight)
+    pr.hp.update(beta1=beta1, beta2=beta2, eps=eps)
+    check_step(pr, 0.8, 1)
+    check_step(pr, None, 2)
 
 
 def test_bias_correction_off_and_decay_off():
@@ -355,6 +369,25 @@ def test_v_above_zero_never_reads_as_zero():
     rest = g == g[1]
     assert (v[rest] > 0).all()
     assert p[rest].abs().max() <= 4 * 1e-3 * 1.001
+
+
+def test_more_than_2_to_31_elements_32():
+    n = (1 << 31) + 300
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB of free device memory")
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    total = ob.onebit_adamw_layout([n])[1]
+    m, v = (torch.zeros(total, device=DEV) for _ in range(2))
+    ctl = torch.zeros(8, dtype=torch.int64, device=DEV)
+    tail = 70_000
+    g[-tail:] = (torch.randn(tail, device=DEV) * 1e-2).to(torch.bfloat16)
+    ob.onebit_adamw_step([p], [g], m, v, ctl, 1e-2)
+    (p1, m1, v1), (ep, em, ev) = ref.step64(host(p[-tail:]) * 0, host(g[-tail:]), np.zeros(tail),
+                                            np.zeros(tail), 1, 1e-2, 0.9, 0.999, 1e-8, 0.0)
+    assert (np.abs(host(m[n - tail:n]) - m1) <= em).all()
+    assert (np.abs(host(v[n - tail:n]) - v1) <= ev).all()
+    assert (np.abs(host(p[-tail:]) - p1) <= ref.bf16_bound(p1, ep)).all()
+    assert not p[:-tail].any() and not m[:n - tail].any() and not m[n:].any()
 
 
 def test_more_than_2_to_31_elements():
@@ -568,6 +601,19 @@ def test_refusals_on_the_device():
     assert same_bits(before, pr.everything())
     # gradients may share memory
     pr.step(grads=[pr.g[0], pr.g[0][:300]])
+
+
+def test_autograd_sees_that_parameters_changed():
+    """The step counts as an in-place change of the parameters: a backward pass through values that
+    it overwrote is refused by autograd."""
+    w = torch.randn(1000, device=DEV, requires_grad=True)
+    loss = (w * w).sum()
+    opt = ob.AdamW([w])
+    g = torch.ones_like(w)
+    with torch.no_grad():
+        opt.step([w], [g], 1e-3)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
 
 
 # ----------------------------------------------------------------------------------------------
