@@ -219,8 +219,8 @@ void step(const char* where, const py::object& params, const py::object& grads,
         st[k] = &vector(state[k], eight ? at::kByte : at::kFloat, k < 2 ? total : blocks, names[k],
                         &device);
     std::vector<double> wd;
-    if (PyFloat_Check(decay.ptr()) || PyLong_Check(decay.ptr())) {
-        wd.assign(p.n(), py::cast<double>(decay));
+    if (!PySequence_Check(decay.ptr())) {
+        wd.assign(p.n(), py::cast<double>(py::float_(decay)));
     } else {
         const py::object seq = py::reinterpret_steal<py::object>(
             PySequence_Fast(decay.ptr(), "weight_decay must be a number or a list of numbers"));

@@ -588,7 +588,7 @@ int onebit01_dp_phase(onebit_adam_t h, int32_t phase, float* x, const void* grad
  * Refused (ONEBIT_ERR_ARG, ONEBIT_ERR_ALIGN; the reason in onebit_last_error): what the above
  * excludes; betas outside [0, 1); lr, eps or wd not finite, eps or wd negative; any buffer that is
  * written and overlaps another of the call (the same parameter twice, a gradient in a parameter's
- * memory); gradients may share memory.
+ * memory); gradients may share memory. ONEBIT_ERR_SPACE if the host runs out of memory.
  * ------------------------------------------------------------------------------------------
  */
 #define ONEBIT_ADAMW_BLOCK 256

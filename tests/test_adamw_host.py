@@ -3,6 +3,9 @@
 stochastic rounding."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,8 @@ import torch
 import communication_compressed_optimizer_momentum_b200 as ob
 from adamw_reference import random_words
 from communication_compressed_optimizer_momentum_b200 import _abi
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -208,6 +213,36 @@ def test_binding_refuses_host_tensors_and_wrong_kinds():
         ob.AdamW([])
     with pytest.raises(ValueError, match="f32"):
         ob.AdamW([x], state="f16")
+
+
+MISSING = r'''
+import sys
+sys.path.insert(0, %r)
+import torch
+from communication_compressed_optimizer_momentum_b200 import _abi
+_abi.LIB_PATH = "/nonexistent/libonebit_adam.so"
+import communication_compressed_optimizer_momentum_b200 as ob
+x, q = torch.zeros(256), torch.zeros(256, dtype=torch.uint8)
+for name, fn in {
+        "layout": lambda: ob.onebit_adamw_layout([3]),
+        "step": lambda: ob.onebit_adamw_step([x], [x], x, x, x, 1e-3),
+        "step8": lambda: ob.onebit_adamw8_step([x], [x], q, q, q, q, x, 1e-3),
+        "get": lambda: ob.onebit_adamw8_get_state(q, q, q, q),
+        "set": lambda: ob.onebit_adamw8_set_state(q, q, q, q, x, x),
+        "norm": lambda: ob.onebit_grad_norm([x])}.items():
+    try:
+        fn()
+    except RuntimeError as e:
+        assert "not built" in str(e), (name, str(e))
+        continue
+    raise SystemExit("%%s did not raise" %% name)
+print("all raised")
+''' % ROOT
+
+
+def test_every_function_raises_without_the_library():
+    r = subprocess.run([sys.executable, "-c", MISSING], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "all raised" in r.stdout, r.stdout + r.stderr
 
 
 # ----------------------------------------------------------------------------------------------

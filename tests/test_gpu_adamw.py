@@ -270,7 +270,8 @@ def test_equals_the_warmup_step_and_hands_over_to_one_bit_adam(gdtype):
 @pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
 @pytest.mark.parametrize("scale", [math.inf, -math.inf, math.nan])
 def test_a_scale_that_is_not_finite_leaves_the_step_out(eight, scale):
-    pr = Problem(LONGER, torch.float32, torch.bfloat16, 1, copies=True, eight=eight)
+    pr = Problem(LONGER if scale == math.inf else SHORT, torch.float32, torch.bfloat16, 1,
+                 copies=True, eight=eight)
     pr.set_t(4)
     before = pr.everything()
     pr.step(scale=torch.tensor([scale], device=DEV))
