@@ -451,7 +451,7 @@ __device__ __forceinline__ void adamw8_block(const StepScalars& s, float keep, u
     store_state<kTopV>(a.vc + se, a.vk + sb, lane, len, vv, av);
 }
 
-// The same block with a third of the instructions (103 -> 44 an element), which is what the 8-bit
+// The same block with a third of the instructions (103 -> 43 an element), which is what the 8-bit
 // step is short of: at 10 bytes an element HBM leaves an SM about 42 issue slots. Same results, bit
 // for bit. What makes it short:
 //  - pairs of fp32 operations in one instruction (f32x2);
@@ -727,9 +727,9 @@ struct Out8 {
 // 333.6M parameters, transfers alone: 606 us against 545 without them). The next block but one is
 // loaded while a block is computed, within the 80 registers that let three thread blocks share an
 // SM. Blocks that a unit does not hold in full (tensors' ends) or that are not aligned go one by
-// one. 333.6M parameters, one B200: fp32 with bf16 gradients and copies 868 us (94% of the
-// measured copy bandwidth), all bf16 650 us (79%; 44 instructions an element at 0.7 issued a
-// cycle are as long as the transfers), fp32 at odd addresses 1159 us.
+// one. 333.6M parameters, one B200: all fp32 811 us (101% of the measured copy bandwidth), with
+// bf16 gradients and copies 851 us (96%), all bf16 623-642 us (80-82%; 43 instructions an element
+// at 0.67 issued a cycle take longer than the transfers), fp32 at odd addresses 1133 us (72%).
 template <typename PT, typename GT, int N>
 __global__ void __launch_bounds__(kThreads, kStepBlocks)
 k_adamw8(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
@@ -805,8 +805,8 @@ k_adamw8(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
 }
 
 // The 8-bit states as values, and back (rounded to nearest even): units of kUnit blocks as in the
-// step. 333.6M parameters: to fp32 584 us (87% of the measured copy bandwidth; four bytes written
-// for one read), to bf16 322 us (95%), from fp32 495 us (103%).
+// step; all of m's values before v's, so that a warp writes 4 KB at a time. 333.6M parameters: to
+// fp32 496 us (103% of the measured copy bandwidth), to bf16 295 us (104%), from fp32 484 us (105%).
 template <int TOP>
 __device__ __forceinline__ void decode8(uint2 w, uint32_t k, float (&x)[8]) {
     float f1, f2;
@@ -866,29 +866,36 @@ k_adamw8_get(const uint8_t* mc, const uint8_t* vc, const uint8_t* mk, const uint
     for (int64_t b = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kUnit; b < nblk;
          b += hop) {
         uint2 cm[kUnit], cv[kUnit];
-        uint32_t km[kUnit], kv[kUnit];
+        uint32_t km = 0u, kv = 0u;
+        const bool full = b + kUnit <= nblk;
 #pragma unroll
         for (int q = 0; q < kUnit; ++q) {
             const bool in = b + q < nblk;
             const int64_t e = (b + q) * kBlk + lane * kBlkLane;
             cm[q] = in && m ? *reinterpret_cast<const uint2*>(mc + e) : make_uint2(0u, 0u);
             cv[q] = in && v ? *reinterpret_cast<const uint2*>(vc + e) : make_uint2(0u, 0u);
-            km[q] = in && m ? mk[b + q] : 0u;
-            kv[q] = in && v ? vk[b + q] : 0u;
+        }
+        if (full) {
+            if (m) km = *reinterpret_cast<const uint32_t*>(mk + b);
+            if (v) kv = *reinterpret_cast<const uint32_t*>(vk + b);
+        } else {
+            for (int q = 0; b + q < nblk; ++q) {
+                if (m) km |= (uint32_t)mk[b + q] << (8 * q);
+                if (v) kv |= (uint32_t)vk[b + q] << (8 * q);
+            }
+        }
+        float x[8];
+#pragma unroll
+        for (int q = 0; q < kUnit; ++q) {
+            if (!m || b + q >= nblk) break;
+            decode8<kTopM>(cm[q], (km >> (8 * q)) & 0xffu, x);
+            st8(m + (b + q) * kBlk + lane * kBlkLane, x);
         }
 #pragma unroll
         for (int q = 0; q < kUnit; ++q) {
-            if (b + q >= nblk) break;
-            const int64_t e = (b + q) * kBlk + lane * kBlkLane;
-            float x[8];
-            if (m) {
-                decode8<kTopM>(cm[q], km[q], x);
-                st8(m + e, x);
-            }
-            if (v) {
-                decode8<kTopV>(cv[q], kv[q], x);
-                st8(v + e, x);
-            }
+            if (!v || b + q >= nblk) break;
+            decode8<kTopV>(cv[q], (kv >> (8 * q)) & 0xffu, x);
+            st8(v + (b + q) * kBlk + lane * kBlkLane, x);
         }
     }
 }
