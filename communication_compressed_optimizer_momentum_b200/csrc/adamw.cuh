@@ -37,20 +37,30 @@ struct Ranges {
     }
     bool clash() {
         const auto by = [](const R& a, const R& b) { return a.lo < b.lo; };
-        size_t at[kRuns] = {};
-        for (auto& run : r)
+        const R *at[kRuns], *end[kRuns];
+        int n = 0;
+        for (auto& run : r) {
+            if (run.empty()) continue;
             if (!std::is_sorted(run.begin(), run.end(), by)) std::sort(run.begin(), run.end(), by);
+            at[n] = run.data();
+            end[n++] = run.data() + run.size();
+        }
         uintptr_t any = 0, written = 0;
-        for (;;) {
-            int k = -1;
-            for (int j = 0; j < kRuns; ++j)
-                if (at[j] < r[j].size() && (k < 0 || r[j][at[j]].lo < r[k][at[k]].lo)) k = j;
-            if (k < 0) return false;
-            const R& x = r[k][at[k]++];
+        while (n > 0) {
+            int k = 0;
+            for (int j = 1; j < n; ++j)
+                if (at[j]->lo < at[k]->lo) k = j;
+            const R& x = *at[k];
             if (x.lo < written || (x.write && x.lo < any)) return true;
             any = std::max(any, x.hi);
             if (x.write) written = std::max(written, x.hi);
+            if (++at[k] == end[k]) {
+                --n;
+                at[k] = at[n];
+                end[k] = end[n];
+            }
         }
+        return false;
     }
 };
 
@@ -122,15 +132,19 @@ int32_t fill(const TensorList& l, int32_t i, int64_t blk0, TensorTable<N>& t) {
     for (; i < l.n && t.n < N; ++i) {
         const int64_t n = l.numel[i];
         if (n == 0) continue;
-        const uint64_t nb = (uint64_t)ceil_div(n, kBlk);
-        if (b + nb > 0x80000000ull) break;
+        // the norm (no parameters) counts blocks from the vector that the tensor begins in
+        const int64_t w = width(l.gtype);
+        const int64_t lead =
+            l.p == nullptr ? (int64_t)(reinterpret_cast<uintptr_t>(l.g[i]) % (8 * w)) / w : 0;
+        const uint64_t nb = (uint64_t)ceil_div(n + lead, kBlk);
+        if (t.n > 0 && b + nb > 0x80000000ull) break;
         const int k = t.n++;
         t.first[k] = (uint32_t)b;
-        t.g[k] = l.g[i];
+        t.g[k] = static_cast<const char*>(l.g[i]) - lead * w;
         t.p[k] = l.p != nullptr ? l.p[i] : nullptr;
         t.c[k] = l.c != nullptr ? l.c[i] : nullptr;
         t.wd[k] = l.wd != nullptr ? l.wd[i] : 0.0;
-        t.last[k] = (uint16_t)(n - (int64_t)(nb - 1) * kBlk);
+        t.last[k] = (uint16_t)((n + lead - (int64_t)(nb - 1) * kBlk) | lead << kTabShift);
         if (aligned_to(t.g[k], 8 * width(l.gtype)) && aligned_to(t.p[k], 8 * width(l.ptype)) &&
             aligned16(t.c[k]))
             t.last[k] |= kTabVec;

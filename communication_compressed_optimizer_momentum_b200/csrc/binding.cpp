@@ -107,7 +107,7 @@ List list_of(const py::handle& o, const char* name, const c10::Device* device,
     c10::Device first(c10::kCPU);
     for (Py_ssize_t i = 0; i < n; ++i) {
         PyObject* p = PySequence_Fast_GET_ITEM(l.seq.ptr(), i);
-        if (!THPVariable_Check(p))
+        if (!THPVariable_CheckExact(p) && !THPVariable_Check(p))
             throw py::type_error(std::string(name) + " must be a list of tensors");
         const at::Tensor& t = THPVariable_Unpack(p);
         if (i == 0) {

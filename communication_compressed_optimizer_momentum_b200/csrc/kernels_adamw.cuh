@@ -23,7 +23,11 @@ constexpr int kBlkLane = kBlk / 32;   // of one lane
 constexpr int kStepBlocks = 3;        // thread blocks per SM of the steps: 80 registers a thread
 constexpr int kUnit = 4;              // blocks that a warp of the 8-bit step takes at a time
 constexpr uint32_t kGolden = 0x9E3779B9u;
-constexpr uint16_t kTabVec = 0x8000u;  // TensorTable::last: all addresses take ld8 and st8
+// TensorTable::last: elements in the last block (9 bits), elements of the first block that lie
+// before the tensor (3 bits; the norm's blocks begin at addresses that take ld8), and whether all
+// addresses take ld8 and st8.
+constexpr int kTabShift = 9;
+constexpr uint16_t kTabVec = 0x8000u;
 
 // The tensors of one launch (empty ones left out).
 template <int N>
@@ -32,7 +36,7 @@ struct TensorTable {
     uint32_t nblk;           // blocks of all tensors
     int64_t blk0;            // state block of the first
     uint32_t first[N + 1];   // first block of each tensor, counted from blk0
-    uint16_t last[N];        // elements in its last block (1..256), kTabVec
+    uint16_t last[N];        // see kTabShift, kTabVec
     void* p[N];              // parameters
     const void* g[N];        // gradients
     void* c[N];              // bf16 copies (or null)
@@ -155,6 +159,12 @@ __device__ __forceinline__ int tensor_of(const TensorTable<N>& t, uint32_t b) {
     return lo;
 }
 
+// Elements of tensor i's first block that lie before it.
+template <int N>
+__device__ __forceinline__ int lead_in(const TensorTable<N>& t, int i) {
+    return (t.last[i] >> kTabShift) & 7;
+}
+
 // A warp's turn: kUnit blocks that begin at a multiple of it (`lead`: blocks before the launch's
 // first within its unit), or what there is of them. i: the tensor of the first, carried along.
 template <int N>
@@ -166,7 +176,8 @@ struct Unit {
         n = min((u + 1) * kUnit - lead, t.nblk) - b;
         while (b >= t.first[i + 1]) ++i;
         const uint32_t full = t.first[i + 1] - ((t.last[i] & 0x1ff) == kBlk ? 0u : 1u);
-        whole = n == kUnit && b + n <= full && (t.last[i] & kTabVec);
+        whole = n == kUnit && b + n <= full && (t.last[i] & kTabVec) &&
+                b >= t.first[i] + (lead_in(t, i) ? 1u : 0u);
     }
 };
 template <int N>
@@ -209,7 +220,7 @@ __device__ __forceinline__ float keep_of(const StepArgs& a, double wd) {
 
 // Count the step once every block of its last launch is done. Only reads of ctl have to come
 // before this, and every thread has used what it read by the barrier: no fence (which small calls
-// feel: 240 tensors of 1 to 4 thousand elements, 6.4 us with one).
+// feel: 240 tensors of 1 to 4 thousand elements take 6.2 us with one, 5.7 without).
 __device__ __forceinline__ void step_done(const StepArgs& a, bool skip) {
     if (!a.advance) return;
     __syncthreads();
@@ -245,9 +256,9 @@ __device__ __forceinline__ float adam_param(const StepScalars& s, const StepArgs
 // 32-bit states
 
 template <bool VEC, typename PT, typename GT>
-__device__ __forceinline__ void adamw_block(const StepScalars& s, const StepArgs& a, float keep, PT* p, const GT* g,
-                                            __nv_bfloat16* c, float* m, float* v, int lane,
-                                            int len) {
+__device__ __forceinline__ void adamw_block(const StepScalars& s, const StepArgs& a, float keep,
+                                            PT* p, const GT* g, __nv_bfloat16* c, float* m,
+                                            float* v, int lane, int len) {
     float pv[8], gv[8], mv[8], vv[8];
     load<VEC>(g, lane, len, gv);
     load<VEC>(m, lane, len, mv);
@@ -264,6 +275,11 @@ __device__ __forceinline__ void adamw_block(const StepScalars& s, const StepArgs
     if (c) store<VEC>(c, lane, len, pv);
 }
 
+// Bound by HBM: 28 bytes a parameter (fp32, bf16 gradients and copies) and 51 instructions, at 0.33
+// issued a cycle. A block a warp at a time; the warps that run at once supply the loads in flight.
+// 333.6M parameters, one B200: all fp32 1400 us (102% of the measured copy bandwidth), with bf16
+// gradients and copies 1455 us (98%), all bf16 1145 us (98%), all bf16 at odd addresses, where
+// elements are accessed one by one, 1350 us (83%).
 template <typename PT, typename GT, int N>
 __global__ void __launch_bounds__(kThreads, kStepBlocks)
 k_adamw(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
@@ -316,7 +332,6 @@ k_adamw(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
 // the ratio below which m reads as 0.
 
 constexpr int kTopM = 15, kTopV = 31;
-
 constexpr uint32_t kExpNan = 255u;
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -974,7 +989,9 @@ __device__ __forceinline__ double sumsq8(const T& raw, double acc) {
 
 // Units as in the 8-bit step: four loads in flight, and the walk over the tensors once for four
 // blocks. bf16, 665M elements: 213 us, 96% of the measured copy bandwidth (block by block 270: the
-// walk and the conversions to fp64 bound it); fp32, 333.6M: 196 us, 104%.
+// walk and the conversions to fp64 bound it); fp32, 333.6M: 196 us, 104%. The blocks are counted
+// from the address before a tensor that takes vector loads, so that views at odd addresses are read
+// as fast (333.6M element by element: bf16 254 us, fp32 316).
 template <typename GT, int N>
 __global__ void __launch_bounds__(kThreads, kNormPerSm)
 k_grad_norm(const __grid_constant__ TensorTable<N> t, const NormArgs a) {
@@ -999,11 +1016,22 @@ k_grad_norm(const __grid_constant__ TensorTable<N> t, const NormArgs a) {
             int k = i;
             for (uint32_t b = at.b; b < at.b + at.n; ++b) {
                 while (b >= t.first[k + 1]) ++k;
+                const int lo = b == t.first[k] ? lead_in(t, k) : 0;
                 const int len = b + 1 == t.first[k + 1] ? t.last[k] & 0x1ff : kBlk;
-                Raw8<float> x;
-                load<false>(static_cast<const GT*>(t.g[k]) + (int64_t)(b - t.first[k]) * kBlk, lane,
-                            len, x.x);
-                acc = sumsq8(x, acc);
+                const GT* g = static_cast<const GT*>(t.g[k]) + (int64_t)(b - t.first[k]) * kBlk;
+                if (lo == 0 && len == kBlk) {
+                    Raw8<GT> x;
+                    x.load(g + lane * kBlkLane);
+                    acc = sumsq8(x, acc);
+                } else {
+                    Raw8<float> x;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = j * 32 + lane;
+                        x.x[j] = e >= lo && e < len ? ld1(g + e) : 0.0f;
+                    }
+                    acc = sumsq8(x, acc);
+                }
             }
         }
     }

@@ -650,7 +650,8 @@ int onebit_adamw8_set_state(int64_t total, uint8_t* m, uint8_t* v, uint8_t* m_ex
                             const float* m_in, const float* v_in, void* stream);
 
 /*
- * The l2 norm over all gradients of a list (fp64 sums of squares in a fixed order) and the factor
+ * The l2 norm over all gradients of a list (fp64 sums of squares, in an order that the lengths and the
+ * addresses modulo 32 fix) and the factor
  * that clips it: work (device, ONEBIT_GRAD_NORM_BYTES, 8-byte aligned, zero-filled before its first
  * call) receives double sum of squares, float norm, float scale = min(1, max_norm / norm), or NaN
  * if the norm is not finite. max_norm > 0, infinity for no clipping. accumulate = 1 adds to the sum

@@ -196,6 +196,16 @@ def test_step_over_long_lists(sizes, eight):
 
 
 @pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
+@pytest.mark.parametrize("first", [1, 300, 600, 800])
+def test_second_launch_begins_anywhere_in_a_unit(first, eight):
+    """More than 800 tensors take two launches; the second one's first block falls on each place
+    among the four blocks that a warp takes at a time, with large aligned tensors behind it."""
+    pr = Problem([first] + [100] * 802 + [5000, 70_001, 4096], torch.float32, torch.float32, 16,
+                 seed=first, eight=eight)
+    check_step(pr, 0.5, 3)
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
 def test_step_without_elements_counts(eight):
     pr = Problem([0, 0], torch.float32, torch.float32, eight=eight)
     check_step(pr, 0.5, 3)
@@ -286,8 +296,8 @@ def test_a_scale_that_is_not_finite_leaves_the_step_out(eight, scale):
 def test_bad_gradients_32(bad, align):
     """One element's gradient is not finite: that element's moments and parameter are not either,
     every other one is as if nothing had happened."""
-    a = Problem([3000, 500], torch.float32, torch.float32, align, seed=2)
-    b = Problem([3000, 500], torch.float32, torch.float32, align, seed=2)
+    a = Problem([2500, 500], torch.float32, torch.float32, align, seed=2)
+    b = Problem([2500, 500], torch.float32, torch.float32, align, seed=2)
     a.g[0][777] = bad
     a.step()
     b.step()
@@ -301,21 +311,21 @@ def test_bad_gradients_32(bad, align):
 def test_bad_gradients_8(bad, align):
     """With 8-bit states the element's whole block of m and v reads as NaN afterwards; the
     parameters of this step and every other block are as if nothing had happened."""
-    a = Problem([3000, 500], torch.float32, torch.float32, align, seed=2, eight=True)
-    b = Problem([3000, 500], torch.float32, torch.float32, align, seed=2, eight=True)
-    for i in (777, 2999):                          # in a whole block and in the last one
+    a = Problem([2500, 500], torch.float32, torch.float32, align, seed=2, eight=True)
+    b = Problem([2500, 500], torch.float32, torch.float32, align, seed=2, eight=True)
+    for i in (777, 2499):                          # in a whole block and in the last one
         a.g[0][i] = bad
     a.step()
     b.step()
     m, v = ob.onebit_adamw8_get_state(*a.state)
     hit = torch.zeros(a.total, dtype=torch.bool, device=DEV)
     hit[768:1024] = True
-    hit[2816:3072] = True
+    hit[2304:2560] = True
     assert m[hit].isnan().all() and v[hit].isnan().all()
     for x, y in zip((m, v), ob.onebit_adamw8_get_state(*b.state)):
         assert torch.equal(x[~hit], y[~hit])
-    assert a.p[0][[777, 2999]].isnan().all()
-    a.p[0][[777, 2999]] = b.p[0][[777, 2999]]
+    assert a.p[0][[777, 2499]].isnan().all()
+    a.p[0][[777, 2499]] = b.p[0][[777, 2499]]
     assert same_bits([a.p_arena], [b.p_arena])
 
 
