@@ -80,7 +80,7 @@ def onebit_adamw_step(params, grads, m, v, ctl, lr, beta1: float = 0.9, beta2: f
     grad_scale: a float32 CUDA tensor of one element that multiplies every gradient; the step is
     left out if it is not finite."""
     _binding().step("onebit_adamw_step", params, grads, (m, v), ctl, lr, beta1, beta2, eps,
-                    weight_decay, copies, grad_scale, bias_correction, stream, None, None)
+                    weight_decay, copies, grad_scale, bias_correction, stream, None, None, None)
 
 
 def onebit_adamw8_step(params, grads, m, v, m_exp, v_exp, ctl, lr, beta1: float = 0.9,
@@ -92,7 +92,7 @@ def onebit_adamw8_step(params, grads, m, v, m_exp, v_exp, ctl, lr, beta1: float 
     random bits of the stochastic rounding."""
     _binding().step("onebit_adamw8_step", params, grads, (m, v, m_exp, v_exp), ctl, lr, beta1,
                     beta2, eps, weight_decay, copies, grad_scale, bias_correction, stream, seed,
-                    None)
+                    None, None)
 
 
 def onebit_adamw8_get_state(m, v, m_exp, v_exp, m_out=None, v_out=None, dtype=None, stream=None):
@@ -120,9 +120,9 @@ class AdamW:
     """AdamW of one parameter list: the states (32-bit, or 8-bit with ``state="q8"``), the step
     count and the buffers of the gradient norm.
 
-    ``step(params, grads, lr)`` clips to ``max_norm`` if one is given (the norm, the factor and the
-    skipping of a step whose norm is not finite stay on the device) and updates every tensor in one
-    launch. The parameters are the caller's; they are passed at every step."""
+    ``step(params, grads, lr)`` clips to ``max_norm`` if one is given (one launch for the norm; the
+    norm, the factor and the skipping of a step whose norm is not finite stay on the device) and
+    updates every tensor in one launch. The parameters are the caller's; they are passed at every step."""
 
     def __init__(self, params, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                  weight_decay=0.01, max_norm=None, state: str = "f32", seed: int = 0,
@@ -153,15 +153,11 @@ class AdamW:
         self.work = zeros(NORM_BYTES, torch.uint8)
 
     def step(self, params, grads, lr, copies=None, grad_scale=None, stream=None) -> None:
-        if self.max_norm is not None:
-            if grad_scale is not None:
-                raise ValueError("grad_scale and max_norm exclude each other")
-            grad_scale = onebit_grad_norm(grads, self.max_norm, self.work, stream=stream)[1]
         _binding().step(
             "onebit_adamw8_step" if self.eight else "onebit_adamw_step", params, grads,
             self._state(), self.ctl, lr, self.beta1, self.beta2, self.eps, self.weight_decay, copies,
             grad_scale, self.bias_correction, stream, self.seed if self.eight else None,
-            self.lengths)
+            self.lengths, None if self.max_norm is None else (self.work, self.max_norm))
 
     @property
     def norm(self):

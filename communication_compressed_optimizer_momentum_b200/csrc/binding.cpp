@@ -26,6 +26,7 @@ decltype(&onebit_adamw8_get_state) p_get = nullptr;
 decltype(&onebit_adamw8_set_state) p_set = nullptr;
 decltype(&onebit_grad_norm) p_norm = nullptr;
 PyObject* g_error = nullptr;  // OneBitError
+constexpr int kScaleOffset = 12;  // of the clip factor in the norm's work, in bytes
 
 template <typename F>
 void address(F& f, const py::dict& d, const char* name) {
@@ -181,12 +182,13 @@ int64_t blocks_of(const std::vector<int64_t>& numel) {
 }
 
 // seed None: fp32 states (m, v); else 8-bit ones (m, v, m_exp, v_exp). lengths: None, or what the
-// parameters' lengths have to be.
+// parameters' lengths have to be. clip: None, or (work, max_norm): the gradients' norm first, whose
+// factor is the step's grad_scale; the lists are read once for both.
 void step(const char* where, const py::object& params, const py::object& grads,
           const py::tuple& state, const py::object& ctl_o, const py::object& lr_o, double beta1,
           double beta2, double eps, const py::object& decay, const py::object& copies,
           const py::object& scale_o, bool bias, const py::object& stream, const py::object& seed,
-          const py::object& lengths) {
+          const py::object& lengths, const py::object& clip) {
     const bool eight = !seed.is_none();
     const Py_ssize_t np = PyObject_Length(params.ptr()), ng = PyObject_Length(grads.ptr());
     if (np < 0 || ng < 0) throw py::error_already_set();
@@ -197,8 +199,14 @@ void step(const char* where, const py::object& params, const py::object& grads,
         vector(ctl_o, at::kLong, ONEBIT_ADAMW_CTL_BYTES / 8, "ctl", nullptr);
     const c10::Device device = ctl.device();
     const List p = list_of(params, "params", &device, nullptr);
-    if (!lengths.is_none() && py::cast<std::vector<int64_t>>(lengths) != p.numel)
-        throw py::value_error("params have lengths other than the optimizer's");
+    if (!lengths.is_none()) {
+        const py::list want = py::cast<py::list>(lengths);
+        bool same = (int64_t)want.size() == p.n();
+        for (int32_t i = 0; same && i < p.n(); ++i)
+            same = PyLong_AsLongLong(PyList_GET_ITEM(want.ptr(), i)) == p.numel[i];
+        if (PyErr_Occurred()) throw py::error_already_set();
+        if (!same) throw py::value_error("params have lengths other than the optimizer's");
+    }
     const List g = list_of(grads, "grads", &device, &p.numel);
     const int32_t pt = dtype_code(p.type, "params"), gt = dtype_code(g.type, "grads");
     List c;
@@ -233,7 +241,15 @@ void step(const char* where, const py::object& params, const py::object& grads,
             throw py::value_error(std::to_string(wd.size()) + " weight decays for " +
                                   std::to_string(np) + " parameters");
     }
-    at::Tensor scale, lr_dev;
+    at::Tensor scale, lr_dev, work;
+    double max_norm = 0.0;
+    if (!clip.is_none()) {
+        if (!scale_o.is_none())
+            throw py::value_error("grad_scale and max_norm exclude each other");
+        const py::tuple both = py::cast<py::tuple>(clip);
+        work = vector(both[0], at::kByte, ONEBIT_GRAD_NORM_BYTES, "work", &device);
+        max_norm = py::cast<double>(both[1]);
+    }
     if (!scale_o.is_none()) scale = vector(scale_o, at::kFloat, 1, "grad_scale", &device);
     double lr = 0.0;
     if (THPVariable_Check(lr_o.ptr()))
@@ -241,12 +257,18 @@ void step(const char* where, const py::object& params, const py::object& grads,
     else
         lr = py::cast<double>(lr_o);
     const auto* scale_p = scale.defined() ? scale.data_ptr<float>() : nullptr;
+    if (work.defined())
+        scale_p = reinterpret_cast<const float*>(work.data_ptr<uint8_t>() + kScaleOffset);
     const auto* lr_p = lr_dev.defined() ? lr_dev.data_ptr<double>() : nullptr;
     void* const* cp = copies.is_none() ? nullptr : c.data.data();
     const uint64_t key = eight ? PyLong_AsUnsignedLongLongMask(seed.ptr()) : 0;
     if (PyErr_Occurred()) throw py::error_already_set();
 
     const Queue q(device, stream);
+    if (work.defined())
+        refuse(p_norm(g.n(), g.numel.data(), g.data.data(), gt, max_norm, 0, work.data_ptr(),
+                      q.handle()),
+               "onebit_grad_norm");
     const int rc =
         eight ? p_step8(p.n(), p.numel.data(), p.data.data(), pt, g.data.data(), gt, cp,
                         st[0]->data_ptr<uint8_t>(), st[1]->data_ptr<uint8_t>(),
@@ -266,6 +288,7 @@ void step(const char* where, const py::object& params, const py::object& grads,
     q.uses(ctl);
     q.uses(scale);
     q.uses(lr_dev);
+    q.uses(work);
 }
 
 // The 8-bit states of one call.
@@ -356,7 +379,7 @@ py::tuple grad_norm(const py::object& grads, double max_norm, const py::object& 
            "onebit_grad_norm");
     q.uses(g.tensors);
     q.uses(work);
-    const at::Tensor both = work.slice(0, 8, 16).view(at::kFloat);
+    const at::Tensor both = work.slice(0, kScaleOffset - 4, kScaleOffset + 4).view(at::kFloat);
     return py::make_tuple(both.select(0, 0), both.select(0, 1));
 }
 

@@ -606,6 +606,13 @@ def test_refusals_on_the_device():
             (step(weight_decay=-1.0), ob.OneBitError, "decay")]:
         with pytest.raises(kind, match=why):
             call()
+    opt = ob.AdamW(pr.p, max_norm=1.0)
+    with pytest.raises(ValueError, match="exclude"):
+        opt.step(pr.p, pr.g, 1e-3, grad_scale=torch.ones(1, device=DEV))
+    with pytest.raises(ValueError, match="optimizer's"):
+        opt.step(pr.p[::-1], pr.g[::-1], 1e-3)
+    with pytest.raises(ob.OneBitError, match="max_norm"):
+        ob.AdamW(pr.p, max_norm=-1.0).step(pr.p, pr.g, 1e-3)
     with pytest.raises(ValueError, match="multiple of 256"):
         ob.onebit_adamw8_get_state(*[torch.zeros(100, dtype=torch.uint8, device=DEV)] * 4)
     torch.cuda.synchronize()
