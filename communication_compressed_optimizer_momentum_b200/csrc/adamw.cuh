@@ -19,8 +19,8 @@ constexpr int kSms = 148;
 
 // Half-open address ranges of one call: what it writes must not overlap anything else, or the
 // result would depend on the order in which the blocks run. Ranges come in runs (a list of
-// tensors each), which are in ascending order in most programs: then one merge settles it, and
-// nothing is sorted (1000 ranges: 2 us against 20).
+// tensors each), which are nearly in ascending order in most programs: merges settle it, and
+// nothing is sorted (a step over 800 separately allocated tensors: 49 us, against 55 sorted).
 struct Ranges {
     struct R {
         uintptr_t lo, hi;
@@ -35,13 +35,32 @@ struct Ranges {
             r[run].push_back({lo, lo + (uintptr_t)bytes, write});
         }
     }
+    static bool by(const R& a, const R& b) { return a.lo < b.lo; }
+    // Ascending order by merging what is in order already: allocators give addresses in few runs.
+    static void order(std::vector<R>& v) {
+        std::vector<size_t> cut{0};
+        for (size_t i = 1; i < v.size(); ++i)
+            if (by(v[i], v[i - 1])) cut.push_back(i);
+        if (cut.size() > 16) return std::sort(v.begin(), v.end(), by);
+        cut.push_back(v.size());
+        while (cut.size() > 2) {
+            std::vector<size_t> next;
+            size_t k = 0;
+            for (; k + 2 < cut.size(); k += 2) {
+                std::inplace_merge(v.begin() + cut[k], v.begin() + cut[k + 1],
+                                   v.begin() + cut[k + 2], by);
+                next.push_back(cut[k]);
+            }
+            for (; k < cut.size(); ++k) next.push_back(cut[k]);
+            cut.swap(next);
+        }
+    }
     bool clash() {
-        const auto by = [](const R& a, const R& b) { return a.lo < b.lo; };
         const R *at[kRuns], *end[kRuns];
         int n = 0;
         for (auto& run : r) {
             if (run.empty()) continue;
-            if (!std::is_sorted(run.begin(), run.end(), by)) std::sort(run.begin(), run.end(), by);
+            order(run);
             at[n] = run.data();
             end[n++] = run.data() + run.size();
         }
