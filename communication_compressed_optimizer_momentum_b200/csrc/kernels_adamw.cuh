@@ -961,7 +961,9 @@ k_adamw8_set(uint8_t* mc, uint8_t* vc, uint8_t* mk, uint8_t* vk, int64_t nblk, c
 // blocks' partial sums by the block that finishes last), so the result does not depend on which
 // block that is.
 
-constexpr int kNormPerSm = 4;
+// Thread blocks per SM of the norm: what keeps enough bf16 in flight (665M elements: 216 us with 4,
+// 202 with 6), at fp32's best (194 with 4 and 6, 204 with 5 and 7).
+constexpr int kNormPerSm = 6;
 constexpr int kNormBlocks = 148 * kNormPerSm;
 
 struct NormWork {              // ONEBIT_GRAD_NORM_BYTES; zero before the first call
@@ -988,10 +990,10 @@ __device__ __forceinline__ double sumsq8(const T& raw, double acc) {
 }
 
 // Units as in the 8-bit step: four loads in flight, and the walk over the tensors once for four
-// blocks. bf16, 665M elements: 213 us, 96% of the measured copy bandwidth (block by block 270: the
-// walk and the conversions to fp64 bound it); fp32, 333.6M: 196 us, 104%. The blocks are counted
-// from the address before a tensor that takes vector loads, so that views at odd addresses are read
-// as fast (333.6M element by element: bf16 254 us, fp32 316).
+// blocks. Bound by HBM: bf16, 665M elements: 202 us, 101% of the measured copy bandwidth (block by
+// block 270: the walk; a sustained loop at the power cap 230); fp32, 333.6M: 194 us, 105%. The blocks are counted from the address before a
+// tensor that takes vector loads, so that views at odd addresses are read as fast (333.6M element by
+// element: bf16 254 us, fp32 316).
 template <typename GT, int N>
 __global__ void __launch_bounds__(kThreads, kNormPerSm)
 k_grad_norm(const __grid_constant__ TensorTable<N> t, const NormArgs a) {
