@@ -5,7 +5,8 @@ states of one parameter list.
 The functions check every tensor before its address goes to the library: CUDA, contiguous, of the
 expected type, length and device. Work is queued on ``stream`` (default: the device's current one)
 with the tensors' device current; tensors that are used on another stream than the current one are
-marked as used there, so that their memory is not handed out again too early. The checks are
+marked as used there, so that their memory is not handed out again too early, and results that a
+call allocates are that stream's memory. The order between streams is the caller's. The checks are
 native (``csrc/binding.cpp``, built into ``_binding.so``): a list may hold hundreds of tensors.
 """
 from __future__ import annotations

@@ -163,6 +163,17 @@ class Queue {
         if (stream_.stream() == current_.stream()) return;
         for (const at::Tensor* t : ts) uses(*t);
     }
+    // Memory of the call's own stream for a result. The current stream's pool may hand out a block
+    // that work queued there still uses, which the call's stream does not wait for. The caller goes
+    // on with the result on the current stream: it is marked as used there.
+    template <typename F>
+    at::Tensor make(F&& allocate) const {
+        const c10::cuda::CUDAStreamGuard on(stream_);
+        const at::Tensor t = allocate();
+        if (stream_.stream() != current_.stream() && t.numel() > 0)
+            t.record_stream(current_.unwrap());
+        return t;
+    }
 
   private:
     c10::cuda::CUDAGuard guard_;
@@ -331,8 +342,9 @@ py::tuple get_state8(const py::object& m, const py::object& v, const py::object&
     const py::object* given[2] = {&m_out, &v_out};
     static const char* const names[2] = {"m_out", "v_out"};
     for (int k = 0; k < 2; ++k)
-        out[k] = given[k]->is_none() ? at::empty({s.total}, s.m.options().dtype(type))
-                                     : vector(*given[k], type, s.total, names[k], &device);
+        out[k] = given[k]->is_none()
+                     ? q.make([&] { return at::empty({s.total}, s.m.options().dtype(type)); })
+                     : vector(*given[k], type, s.total, names[k], &device);
     refuse(p_get(s.total, s.m.data_ptr<uint8_t>(), s.v.data_ptr<uint8_t>(),
                  s.mk.data_ptr<uint8_t>(), s.vk.data_ptr<uint8_t>(), out[0].data_ptr(),
                  out[1].data_ptr(), code, q.handle()),
@@ -369,11 +381,10 @@ py::tuple grad_norm(const py::object& grads, double max_norm, const py::object& 
     const int32_t code = dtype_code(g.type, "grads");
     const c10::Device device = work.defined() ? expected : g.tensors[0]->device();
     const Queue q(device, stream);
-    if (!work.defined()) {
-        const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(
-            reinterpret_cast<cudaStream_t>(q.handle()), device.index()));
-        work = at::zeros({ONEBIT_GRAD_NORM_BYTES}, g.tensors[0]->options().dtype(at::kByte));
-    }
+    if (!work.defined())
+        work = q.make([&] {
+            return at::zeros({ONEBIT_GRAD_NORM_BYTES}, g.tensors[0]->options().dtype(at::kByte));
+        });
     refuse(p_norm(g.n(), g.numel.data(), g.data.data(), code, max_norm, accumulate ? 1 : 0,
                   work.data_ptr(), q.handle()),
            "onebit_grad_norm");
