@@ -103,7 +103,9 @@ def onebit_adamw8_get_state(m, v, m_exp, v_exp, m_out=None, v_out=None, dtype=No
 
 
 def onebit_adamw8_set_state(m, v, m_exp, v_exp, m_in, v_in, stream=None) -> None:
-    """Encode float32 values of the states' length into the 8-bit states, rounded to nearest."""
+    """Encode float32 values of the states' length into the 8-bit states, rounded to nearest. All
+    256 values of a block share its exponent: the places behind a tensor have to hold zeros
+    (``AdamW.set_state`` sees to that)."""
     _binding().set_state8(m, v, m_exp, v_exp, m_in, v_in, stream)
 
 
@@ -181,8 +183,22 @@ class AdamW:
             return self.m, self.v
         return onebit_adamw8_get_state(*self._state(), stream=stream)
 
+    def _encodable(self, x):
+        """Flat moments as the 8-bit states take them in: zeros behind the tensors, whose places
+        share a block's exponent with the tensor's last elements. The caller's vector may hold
+        anything there (a copy of the flat states' size, where any tensor ends within a block)."""
+        import torch
+        ends = self.offsets[1:] + [self.total]
+        gaps = [(o + n, end) for o, n, end in zip(self.offsets, self.lengths, ends) if o + n < end]
+        if not gaps:
+            return x
+        x = x[:self.total].clone()
+        torch._foreach_zero_([x[a:b] for a, b in gaps])
+        return x
+
     def set_state(self, m, v, t: int) -> None:
-        """Continue after step t with these flat float32 moments (8-bit states: rounded)."""
+        """Continue after step t with these flat float32 moments (8-bit states: rounded). Their
+        places behind a tensor may hold anything."""
         import torch
         if t < 0:
             raise ValueError("t must be >= 0")
@@ -194,7 +210,7 @@ class AdamW:
                                  dtype=torch.float64).view(torch.int64)
         self.ctl.copy_(host)
         if self.eight:
-            onebit_adamw8_set_state(*self._state(), m, v)
+            onebit_adamw8_set_state(*self._state(), self._encodable(m), self._encodable(v))
         else:
             self.m.copy_(m[:self.total])
             self.v.copy_(v[:self.total])

@@ -641,6 +641,8 @@ int onebit_adamw8_step(int32_t ntensors, const int64_t* numel, void* const* para
  * [total], aligned to 8 values; either may be NULL, both not) receive what the codes stand for, exact
  * in fp32 and bf16 unless below their range. set: codes and exponents from fp32 values, rounded to
  * nearest even; values of v below 0 count as 0. Setting what get returned gives the same values.
+ * Both take the flat states as they are, the places behind the tensors among them: set needs zeros
+ * there, because a block's exponent is that of its largest value wherever it stands.
  * ONEBIT_ERR_ARG where source and destination overlap.
  */
 int onebit_adamw8_get_state(int64_t total, const uint8_t* m, const uint8_t* v,

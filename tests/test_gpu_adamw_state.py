@@ -1,0 +1,59 @@
+"""``AdamW``'s states on their way in and out: what lies behind a tensor, refusals that change
+nothing, and checkpoints."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import communication_compressed_optimizer_momentum_b200 as ob
+import adamw_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BLOCK = 256
+SIZES = [1, 255, 256, 0, 257, 700, 512]
+
+
+def params(sizes=SIZES):
+    return [torch.zeros(n, device=DEV) for n in sizes]
+
+
+def moments(opt, seed=0):
+    """Flat moments with zeros behind the tensors, and where the tensors' own places are."""
+    rng = np.random.default_rng(seed)
+    inside = np.zeros(opt.total, bool)
+    for o, n in zip(opt.offsets, opt.lengths):
+        inside[o:o + n] = True
+    m = np.where(inside, rng.standard_normal(opt.total) * 1e-2, 0.0).astype(np.float32)
+    v = np.where(inside, rng.random(opt.total) * 1e-4, 0.0).astype(np.float32)
+    return m, v, inside
+
+
+@pytest.mark.parametrize("junk", [math.nan, math.inf, 1e30, 77.0])
+@pytest.mark.parametrize("state", ["q8", "f32"])
+def test_what_lies_behind_a_tensor_does_not_count(state, junk):
+    """Moments whose places behind the tensors hold anything: the tensors' elements become what they
+    become with zeros there, the caller's vectors stay as they are, and the next step is the same."""
+    opt, other = (ob.AdamW(params(), state=state, seed=1) for _ in range(2))
+    m, v, inside = moments(opt)
+    dirty = [torch.from_numpy(np.where(inside, x, np.float32(junk))).to(DEV) for x in (m, v)]
+    kept = [x.clone() for x in dirty]
+    opt.set_state(*dirty, 3)
+    assert all(torch.equal(x.view(torch.int32), y.view(torch.int32)) for x, y in zip(dirty, kept))
+    clean = [torch.from_numpy(x).to(DEV) for x in (m, v)]
+    other.set_state(*clean, 3)
+    for x, y, want, signed in zip(opt.get_state(), other.get_state(), (m, v), (True, False)):
+        x, y = x.cpu().numpy(), y.cpu().numpy()
+        assert np.array_equal(x[inside], y[inside])
+        if state == "q8":
+            codes, k = ref.encode64(want, signed)
+            assert np.array_equal(x[inside], ref.decode64(codes, k, signed)[inside])
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    grads = [torch.randn(n, device=DEV, generator=gen) for n in SIZES]
+    p, q = params(), params()
+    opt.step(p, grads, 1e-2)
+    other.step(q, grads, 1e-2)
+    assert all(torch.equal(x, y) for x, y in zip(p, q))
+    assert all(torch.isfinite(x).all() for x in p)
