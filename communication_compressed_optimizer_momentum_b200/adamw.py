@@ -184,16 +184,17 @@ class AdamW:
         return onebit_adamw8_get_state(*self._state(), stream=stream)
 
     def _encodable(self, x):
-        """Flat moments as the 8-bit states take them in: zeros behind the tensors, whose places
-        share a block's exponent with the tensor's last elements. The caller's vector may hold
-        anything there (a copy of the flat states' size, where any tensor ends within a block)."""
+        """Flat moments as the 8-bit states take them in: at an aligned address, and zeros behind the
+        tensors, whose places share a block's exponent with the tensor's last elements. The caller's
+        vector may be a view of any address and hold anything there (a copy of the flat states' size
+        where it is, or where any tensor ends within a block)."""
         import torch
         ends = self.offsets[1:] + [self.total]
         gaps = [(o + n, end) for o, n, end in zip(self.offsets, self.lengths, ends) if o + n < end]
-        if not gaps:
-            return x
-        x = x[:self.total].clone()
-        torch._foreach_zero_([x[a:b] for a, b in gaps])
+        if gaps or x.data_ptr() % 32 != 0:
+            x = x.view(-1)[:self.total].clone()
+        if gaps:
+            torch._foreach_zero_([x[a:b] for a, b in gaps])
         return x
 
     def set_state(self, m, v, t: int) -> None:

@@ -57,3 +57,21 @@ def test_what_lies_behind_a_tensor_does_not_count(state, junk):
     other.step(q, grads, 1e-2)
     assert all(torch.equal(x, y) for x, y in zip(p, q))
     assert all(torch.isfinite(x).all() for x in p)
+
+
+@pytest.mark.parametrize("sizes", [SIZES, [512, 256]], ids=["gaps", "whole_blocks"])
+@pytest.mark.parametrize("state", ["q8", "f32"])
+def test_moments_at_any_address(state, sizes):
+    """Views at addresses that are aligned to one element only, as in a loaded checkpoint."""
+    opt, other = (ob.AdamW(params(sizes), state=state) for _ in range(2))
+    m, v, _ = moments(opt, 4)
+    arena = torch.full((2 * opt.total + 4,), 5.0, device=DEV)
+    views = [arena[1:1 + opt.total], arena[opt.total + 3:2 * opt.total + 3]]
+    clean = [torch.from_numpy(x).to(DEV) for x in (m, v)]
+    for x, y in zip(views, clean):
+        assert x.data_ptr() % 16 != 0
+        x.copy_(y)
+    opt.set_state(*views, 9)
+    other.set_state(*clean, 9)
+    assert all(torch.equal(x, y) for x, y in zip(opt.get_state(), other.get_state()))
+    assert opt.counts() == other.counts() == (9, 0)
