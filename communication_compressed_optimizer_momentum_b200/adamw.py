@@ -209,12 +209,12 @@ class AdamW:
         host[0] = t
         host[2:4] = torch.tensor([1.0 - self.beta1 ** t, 1.0 - self.beta2 ** t],
                                  dtype=torch.float64).view(torch.int64)
-        self.ctl.copy_(host)
         if self.eight:
             onebit_adamw8_set_state(*self._state(), self._encodable(m), self._encodable(v))
         else:
-            self.m.copy_(m[:self.total])
-            self.v.copy_(v[:self.total])
+            self.m.copy_(m.view(-1)[:self.total])
+            self.v.copy_(v.view(-1)[:self.total])
+        self.ctl.copy_(host)                     # last: a call that is refused changes nothing
 
     def checkpoint(self) -> dict:
         """Copies of everything a fresh AdamW of the same list needs to continue bit for bit."""

@@ -75,3 +75,36 @@ def test_moments_at_any_address(state, sizes):
     other.set_state(*clean, 9)
     assert all(torch.equal(x, y) for x, y in zip(opt.get_state(), other.get_state()))
     assert opt.counts() == other.counts() == (9, 0)
+
+
+@pytest.mark.parametrize("state", ["q8", "f32"])
+def test_moments_of_any_shape(state):
+    """Contiguous moments count as flat whatever their shape, and longer ones from their start."""
+    sizes = [300, 256]
+    opt, other = (ob.AdamW(params(sizes), state=state) for _ in range(2))
+    m, v, _ = moments(opt, 5)
+    clean = [torch.from_numpy(x).to(DEV) for x in (m, v)]
+    other.set_state(*clean, 2)
+    opt.set_state(clean[0].view(-1, 256), torch.cat([clean[1], clean[1]]).view(2, -1), 2)
+    assert all(torch.equal(x, y) for x, y in zip(opt.get_state(), other.get_state()))
+    opt.set_state(torch.cat([clean[0], clean[0]]).view(-1, 2), clean[1].view(-1, 1), 2)
+    assert all(torch.equal(x, y) for x, y in zip(opt.get_state(), other.get_state()))
+
+
+def test_a_refused_set_state_changes_nothing():
+    """Moments that lie in the states themselves, which the encoder refuses: the step count stays."""
+    opt = ob.AdamW(params([512, 2048]), state="q8")
+    m, v, _ = moments(opt)
+    opt.set_state(torch.from_numpy(m).to(DEV), torch.from_numpy(v).to(DEV), 6)
+    # 2560 codes and, as fp32, the same memory: a buffer that both begin in
+    arena = torch.zeros(4 * opt.total, dtype=torch.uint8, device=DEV)
+    arena[:opt.total] = opt.m
+    opt.m = arena[:opt.total]
+    before = [x.clone() for x in (*opt._state(), opt.ctl)]
+    with pytest.raises(ob.OneBitError, match="overlap"):
+        opt.set_state(arena.view(torch.float32), torch.from_numpy(v).to(DEV), 11)
+    assert opt.counts() == (6, 0)
+    assert all(torch.equal(x, y) for x, y in zip(before, (*opt._state(), opt.ctl)))
+    with pytest.raises(ValueError, match="holds"):
+        opt.set_state(torch.from_numpy(m).to(DEV)[:-1], torch.from_numpy(v).to(DEV), 11)
+    assert opt.counts() == (6, 0)
