@@ -38,7 +38,8 @@ def _binding():
                 "_binding.so is not built (%s); run "
                 "`python -m communication_compressed_optimizer_momentum_b200.build`" % e)
         names = ("onebit_adamw_step", "onebit_adamw8_step", "onebit_adamw8_get_state",
-                 "onebit_adamw8_set_state", "onebit_grad_norm")
+                 "onebit_adamw8_set_state", "onebit_grad_norm",
+                 "onebit_internal_adamw_clipped_step")
         native.init({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names},
                     _ob().OneBitError)
         _native = native

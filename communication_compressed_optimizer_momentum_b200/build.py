@@ -19,6 +19,7 @@ SOURCES = [os.path.join(SRC_DIR, "onebit_adam.cu")]
 DEPS = SOURCES + [os.path.join(SRC_DIR, "kernels.cuh"), os.path.join(SRC_DIR, "kernels_dp.cuh"),
                   os.path.join(SRC_DIR, "kernels_zero_one.cuh"),
                   os.path.join(SRC_DIR, "kernels_adamw.cuh"), os.path.join(SRC_DIR, "adamw.cuh"),
+                  os.path.join(SRC_DIR, "adamw_clip.h"),
                   os.path.join(INCLUDE, "onebit_adam.h")]
 
 # --fmad=false: no contraction of the method's fp32 multiply-adds (every fp32 operation is one
@@ -65,7 +66,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def build_binding(force: bool = False) -> str:
     """Compile the binding's native part if it is missing or older than its sources."""
-    deps = (BINDING_SOURCE, os.path.join(INCLUDE, "onebit_adam.h"))
+    deps = (BINDING_SOURCE, os.path.join(SRC_DIR, "adamw_clip.h"),
+            os.path.join(INCLUDE, "onebit_adam.h"))
     if not force and os.path.exists(BINDING) and \
             all(os.path.getmtime(BINDING) >= os.path.getmtime(p) for p in deps):
         return BINDING

@@ -3,6 +3,7 @@
 // text and helpers it uses.
 #pragma once
 
+#include "adamw_clip.h"
 #include "kernels_adamw.cuh"
 
 static_assert(sizeof(StepCtl) == ONEBIT_ADAMW_CTL_BYTES, "control block");
@@ -279,8 +280,31 @@ int check_step(const char* where, StepArgs& a, double eps) {
     return ONEBIT_OK;
 }
 
+// The norm that comes before a clipped step.
+struct Clip {
+    double max_norm;
+    void* work;
+    bool* queued;  // set when the norm is on its way
+};
+
+int check_norm(const char* where, double max_norm, const void* work) {
+    if (!(max_norm > 0.0)) return bad(where, "max_norm must be > 0");
+    if (work == nullptr) return bad(where, "null work");
+    if (!aligned_to(work, 8)) return bad(where, "work not aligned", ONEBIT_ERR_ALIGN);
+    return ONEBIT_OK;
+}
+
+int queue_norm(const TensorList& l, const NormArgs& a, cudaStream_t st);
+
+// Every check comes before anything is queued, the norm of a clipped step among it.
 template <bool EIGHT>
-int adamw_step(const char* where, const TensorList& l, StepArgs a, double eps, void* stream) {
+int adamw_step(const char* where, const TensorList& l, StepArgs a, double eps, void* stream,
+               Clip* clip = nullptr) {
+    if (clip != nullptr) {
+        const int rc = check_norm(where, clip->max_norm, clip->work);
+        if (rc != ONEBIT_OK) return rc;
+        a.scale = &static_cast<const NormWork*>(clip->work)->scale;
+    }
     int rc = check_step(where, a, eps);
     if (rc != ONEBIT_OK) return rc;
     if (l.n > 0 && l.p == nullptr) return bad(where, "null list");
@@ -308,9 +332,19 @@ int adamw_step(const char* where, const TensorList& l, StepArgs a, double eps, v
         }
     }
     ranges.add(0, a.ctl, sizeof(StepCtl), true);
-    ranges.add(0, a.scale, 4, false);
+    if (clip != nullptr)
+        ranges.add(0, clip->work, ONEBIT_GRAD_NORM_BYTES, true);
+    else
+        ranges.add(0, a.scale, 4, false);
     ranges.add(0, a.lr_dev, 8, false);
     if (ranges.clash()) return bad(where, "tensors or states overlap");
+    if (clip != nullptr) {
+        *clip->queued = true;
+        const TensorList g{l.n, l.numel, nullptr, ONEBIT_F32, l.g, l.gtype, nullptr, nullptr};
+        rc = queue_norm(g, NormArgs{clip->max_norm, 0, static_cast<NormWork*>(clip->work)},
+                        as_stream(stream));
+        if (rc != ONEBIT_OK) return rc;
+    }
     return l.n <= kTabSmall ? queue_step<EIGHT, kTabSmall>(l, a, as_stream(stream))
                             : queue_step<EIGHT, kTabLarge>(l, a, as_stream(stream));
 }
@@ -371,6 +405,15 @@ int queue_norm(const TensorList& l, NormArgs a, cudaStream_t st) {
         launch(k_grad_norm<GT, N>, grid_for(units, kNormPerSm), t, a, st);
         a.accumulate = 1;
     });
+}
+
+int queue_norm(const TensorList& l, const NormArgs& a, cudaStream_t st) {
+    const bool small = l.n <= kTabSmall;
+    if (l.gtype == ONEBIT_F32)
+        return small ? queue_norm<float, kTabSmall>(l, a, st)
+                     : queue_norm<float, kTabLarge>(l, a, st);
+    return small ? queue_norm<__nv_bfloat16, kTabSmall>(l, a, st)
+                 : queue_norm<__nv_bfloat16, kTabLarge>(l, a, st);
 }
 
 }  // namespace
@@ -479,25 +522,40 @@ int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* 
                      void* stream) {
     return guarded([&]() -> int {
         const char* where = "onebit_grad_norm";
-        if (!(max_norm > 0.0)) return bad(where, "max_norm must be > 0");
         if (accumulate != 0 && accumulate != 1) return bad(where, "accumulate must be 0 or 1");
-        if (work == nullptr) return bad(where, "null work");
-        if (!aligned_to(work, 8)) return bad(where, "work not aligned", ONEBIT_ERR_ALIGN);
+        int rc = check_norm(where, max_norm, work);
+        if (rc != ONEBIT_OK) return rc;
         const TensorList l{ntensors, numel, nullptr, ONEBIT_F32, grads, grad_dtype, nullptr, nullptr};
         Ranges ranges;
         int64_t blocks = 0;
-        const int rc = check_list(where, l, ranges, &blocks);
+        rc = check_list(where, l, ranges, &blocks);
         if (rc != ONEBIT_OK) return rc;
         ranges.add(0, work, ONEBIT_GRAD_NORM_BYTES, true);
         if (ranges.clash()) return bad(where, "work overlaps a gradient");
-        const NormArgs a{max_norm, accumulate, static_cast<NormWork*>(work)};
-        cudaStream_t st = as_stream(stream);
-        const bool small = ntensors <= kTabSmall;
-        if (grad_dtype == ONEBIT_F32)
-            return small ? queue_norm<float, kTabSmall>(l, a, st)
-                         : queue_norm<float, kTabLarge>(l, a, st);
-        return small ? queue_norm<__nv_bfloat16, kTabSmall>(l, a, st)
-                     : queue_norm<__nv_bfloat16, kTabLarge>(l, a, st);
+        return queue_norm(l, NormArgs{max_norm, accumulate, static_cast<NormWork*>(work)},
+                          as_stream(stream));
+    });
+}
+
+int onebit_internal_adamw_clipped_step(const OneBitAdamwClip* c, bool* queued) {
+    return guarded([&]() -> int {
+        StepArgs a = step_args(c->ctl, nullptr, c->lr_dev, c->lr, c->beta1, c->beta2,
+                               c->bias_correction);
+        const TensorList l{c->ntensors, c->numel, c->params, c->param_dtype, c->grads,
+                           c->grad_dtype, c->copies, c->weight_decay};
+        Clip clip{c->max_norm, c->work, queued};
+        *queued = false;
+        if (c->eight) {
+            a.mc = static_cast<uint8_t*>(c->m);
+            a.vc = static_cast<uint8_t*>(c->v);
+            a.mk = c->m_exp;
+            a.vk = c->v_exp;
+            a.seed = c->seed;
+            return adamw_step<true>("onebit_adamw8_step", l, a, c->eps, c->stream, &clip);
+        }
+        a.m = static_cast<float*>(c->m);
+        a.v = static_cast<float*>(c->v);
+        return adamw_step<false>("onebit_adamw_step", l, a, c->eps, c->stream, &clip);
     });
 }
 

@@ -14,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "adamw_clip.h"
 #include "onebit_adam.h"
 
 namespace py = pybind11;
@@ -25,6 +26,7 @@ decltype(&onebit_adamw8_step) p_step8 = nullptr;
 decltype(&onebit_adamw8_get_state) p_get = nullptr;
 decltype(&onebit_adamw8_set_state) p_set = nullptr;
 decltype(&onebit_grad_norm) p_norm = nullptr;
+decltype(&onebit_internal_adamw_clipped_step) p_clipped = nullptr;
 PyObject* g_error = nullptr;  // OneBitError
 constexpr int kScaleOffset = 12;  // of the clip factor in the norm's work, in bytes
 
@@ -39,6 +41,7 @@ void init(const py::dict& addresses, const py::object& error) {
     address(p_get, addresses, "onebit_adamw8_get_state");
     address(p_set, addresses, "onebit_adamw8_set_state");
     address(p_norm, addresses, "onebit_grad_norm");
+    address(p_clipped, addresses, "onebit_internal_adamw_clipped_step");
     g_error = error.inc_ref().ptr();
 }
 
@@ -194,7 +197,7 @@ int64_t blocks_of(const std::vector<int64_t>& numel) {
 
 // seed None: fp32 states (m, v); else 8-bit ones (m, v, m_exp, v_exp). lengths: None, or what the
 // parameters' lengths have to be. clip: None, or (work, max_norm): the gradients' norm first, whose
-// factor is the step's grad_scale; the lists are read once for both.
+// factor is the step's grad_scale; the lists are read and checked once for both.
 void step(const char* where, const py::object& params, const py::object& grads,
           const py::tuple& state, const py::object& ctl_o, const py::object& lr_o, double beta1,
           double beta2, double eps, const py::object& decay, const py::object& copies,
@@ -268,38 +271,70 @@ void step(const char* where, const py::object& params, const py::object& grads,
     else
         lr = py::cast<double>(lr_o);
     const auto* scale_p = scale.defined() ? scale.data_ptr<float>() : nullptr;
-    if (work.defined())
-        scale_p = reinterpret_cast<const float*>(work.data_ptr<uint8_t>() + kScaleOffset);
     const auto* lr_p = lr_dev.defined() ? lr_dev.data_ptr<double>() : nullptr;
     void* const* cp = copies.is_none() ? nullptr : c.data.data();
     const uint64_t key = eight ? PyLong_AsUnsignedLongLongMask(seed.ptr()) : 0;
     if (PyErr_Occurred()) throw py::error_already_set();
 
     const Queue q(device, stream);
-    if (work.defined())
-        refuse(p_norm(g.n(), g.numel.data(), g.data.data(), gt, max_norm, 0, work.data_ptr(),
-                      q.handle()),
-               "onebit_grad_norm");
-    const int rc =
-        eight ? p_step8(p.n(), p.numel.data(), p.data.data(), pt, g.data.data(), gt, cp,
-                        st[0]->data_ptr<uint8_t>(), st[1]->data_ptr<uint8_t>(),
-                        st[2]->data_ptr<uint8_t>(), st[3]->data_ptr<uint8_t>(), ctl.data_ptr(), key,
-                        wd.data(), scale_p, lr_p, lr, beta1, beta2, eps, bias ? 1 : 0, q.handle())
-              : p_step(p.n(), p.numel.data(), p.data.data(), pt, g.data.data(), gt, cp,
-                       st[0]->data_ptr<float>(), st[1]->data_ptr<float>(), ctl.data_ptr(),
-                       wd.data(), scale_p, lr_p, lr, beta1, beta2, eps, bias ? 1 : 0, q.handle());
+    int rc;
+    bool queued = false;   // a refusal queues nothing; what is queued uses its tensors even if it fails
+    if (work.defined()) {
+        OneBitAdamwClip a{};
+        a.ntensors = p.n();
+        a.numel = p.numel.data();
+        a.params = p.data.data();
+        a.param_dtype = pt;
+        a.grads = g.data.data();
+        a.grad_dtype = gt;
+        a.copies = cp;
+        a.m = st[0]->data_ptr();
+        a.v = st[1]->data_ptr();
+        a.eight = eight;
+        if (eight) {
+            a.m_exp = st[2]->data_ptr<uint8_t>();
+            a.v_exp = st[3]->data_ptr<uint8_t>();
+        }
+        a.seed = key;
+        a.ctl = ctl.data_ptr();
+        a.weight_decay = wd.data();
+        a.max_norm = max_norm;
+        a.work = work.data_ptr();
+        a.lr_dev = lr_p;
+        a.lr = lr;
+        a.beta1 = beta1;
+        a.beta2 = beta2;
+        a.eps = eps;
+        a.bias_correction = bias ? 1 : 0;
+        a.stream = q.handle();
+        rc = p_clipped(&a, &queued);
+    } else {
+        rc = eight
+                 ? p_step8(p.n(), p.numel.data(), p.data.data(), pt, g.data.data(), gt, cp,
+                           st[0]->data_ptr<uint8_t>(), st[1]->data_ptr<uint8_t>(),
+                           st[2]->data_ptr<uint8_t>(), st[3]->data_ptr<uint8_t>(), ctl.data_ptr(),
+                           key, wd.data(), scale_p, lr_p, lr, beta1, beta2, eps, bias ? 1 : 0,
+                           q.handle())
+                 : p_step(p.n(), p.numel.data(), p.data.data(), pt, g.data.data(), gt, cp,
+                          st[0]->data_ptr<float>(), st[1]->data_ptr<float>(), ctl.data_ptr(),
+                          wd.data(), scale_p, lr_p, lr, beta1, beta2, eps, bias ? 1 : 0,
+                          q.handle());
+        queued = rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA;
+    }
+    if (queued) {
+        changed(p.tensors);
+        changed(c.tensors);
+        q.uses(p.tensors);
+        q.uses(g.tensors);
+        q.uses(c.tensors);
+        for (const at::Tensor* t : st)
+            if (t != nullptr) q.uses(*t);
+        q.uses(ctl);
+        q.uses(scale);
+        q.uses(lr_dev);
+        q.uses(work);
+    }
     refuse(rc, where);
-    changed(p.tensors);
-    changed(c.tensors);
-    q.uses(p.tensors);
-    q.uses(g.tensors);
-    q.uses(c.tensors);
-    for (const at::Tensor* t : st)
-        if (t != nullptr) q.uses(*t);
-    q.uses(ctl);
-    q.uses(scale);
-    q.uses(lr_dev);
-    q.uses(work);
 }
 
 // The 8-bit states of one call.

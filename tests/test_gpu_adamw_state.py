@@ -108,3 +108,48 @@ def test_a_refused_set_state_changes_nothing():
     with pytest.raises(ValueError, match="holds"):
         opt.set_state(torch.from_numpy(m).to(DEV)[:-1], torch.from_numpy(v).to(DEV), 11)
     assert opt.counts() == (6, 0)
+
+
+@pytest.mark.parametrize("side", [False, True], ids=["current", "side"])
+@pytest.mark.parametrize("state", ["q8", "f32"])
+def test_a_refused_clipped_step_changes_nothing(state, side):
+    """Whatever the step refuses, it refuses before the norm of its gradients is taken."""
+    n = 5000
+    arena = torch.zeros(2 * n + 4096, device=DEV)
+    p = [arena[:n], arena[n:2 * n]]
+    g = [torch.randn(n, device=DEV) for _ in p]
+    opt = ob.AdamW(p, weight_decay=0.01, max_norm=1.0, state=state)
+    opt.step(p, g, 1e-2)
+    norm = float(opt.norm)
+    assert abs(norm - float(torch.cat(g).double().norm())) <= 1e-6 * norm
+    torch.cuda.synchronize()
+    before = [x.clone() for x in (arena, opt.work, opt.ctl, *opt._state())]
+    versions = [x._version for x in p]
+    other = [x * 2 for x in g]
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+
+    def refused(why, params=p, lr=1e-2, **change):
+        kept = {name: getattr(opt, name) for name in change}
+        for name, x in change.items():
+            setattr(opt, name, x)
+        with pytest.raises(ob.OneBitError, match=why):
+            opt.step(params, other, lr, stream=stream)
+        for name, x in kept.items():
+            setattr(opt, name, x)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x.view(-1).view(torch.uint8), y.view(-1).view(torch.uint8))
+                   for x, y in zip(before, (arena, opt.work, opt.ctl, *opt._state())))
+        assert float(opt.norm) == norm and [x._version for x in p] == versions
+    refused("lr", lr=math.nan)
+    refused("beta", beta2=1.0)
+    refused("eps", eps=-1.0)
+    refused("decay", weight_decay=-0.1)
+    refused("max_norm", max_norm=-1.0)
+    refused("overlap", params=[p[0], p[0]])
+    refused("overlap", params=[p[0], other[1]])
+    refused("overlap", ctl=arena[:16].view(torch.int64))
+    # a norm's buffer that begins among the parameters' last elements and ends behind them
+    refused("overlap", work=arena[2 * n - 64:2 * n + 4032].view(torch.uint8))
+    opt.step(p, other, 1e-2)
+    assert float(opt.norm) == pytest.approx(2 * norm, rel=1e-6) and opt.counts() == (2, 0)
