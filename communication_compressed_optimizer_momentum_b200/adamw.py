@@ -11,6 +11,7 @@ native (``csrc/binding.cpp``, built into ``_binding.so``): a list may hold hundr
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import List, Sequence, Tuple
@@ -126,7 +127,11 @@ class AdamW:
 
     ``step(params, grads, lr)`` clips to ``max_norm`` if one is given (one launch for the norm; the
     norm, the factor and the skipping of a step whose norm is not finite stay on the device) and
-    updates every tensor in one launch. The parameters are the caller's; they are passed at every step."""
+    updates every tensor in one launch. The parameters are the caller's; they are passed at every step.
+
+    Every method that reads or writes the states takes a ``stream`` (default: the device's current
+    one) and is ordered by it alone: a program that uses several streams makes each wait for the one
+    before, first for the one the optimizer was made on. ``counts`` waits for all of them."""
 
     def __init__(self, params, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                  weight_decay=0.01, max_norm=None, state: str = "f32", seed: int = 0,
@@ -170,12 +175,36 @@ class AdamW:
         return self.work[8:12].view(torch.float32)[0]
 
     def counts(self) -> Tuple[int, int]:
-        """(steps taken, steps left out); waits for the device."""
+        """(steps taken, steps left out); waits for everything that is queued on the device."""
+        import torch
+        torch.cuda.synchronize(self.device)
         t, skipped = self.ctl[:2].tolist()
         return t, skipped
 
     def _state(self):
         return (self.m, self.v, self.m_exp, self.v_exp) if self.eight else (self.m, self.v)
+
+    @contextlib.contextmanager
+    def _on(self, stream, given=()):
+        """``stream`` as the current one, and the states and the tensors given marked as used there;
+        yields the stream that was current."""
+        import torch
+        current = torch.cuda.current_stream(self.device)
+        if stream is None:
+            stream = current
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, self.device) if stream else \
+                torch.cuda.default_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError("stream is on %s, the states are on %s" % (stream.device, self.device))
+        try:
+            with torch.cuda.stream(stream):
+                yield current
+        finally:
+            if stream != current:
+                for x in (*self._state(), self.ctl, *given):
+                    if x.is_cuda and x.numel() > 0:
+                        x.record_stream(stream)
 
     def get_state(self, stream=None):
         """Flat float32 (m, v), tensor i at [offsets[i], offsets[i] + lengths[i]): the states
@@ -198,7 +227,7 @@ class AdamW:
             torch._foreach_zero_([x[a:b] for a, b in gaps])
         return x
 
-    def set_state(self, m, v, t: int) -> None:
+    def set_state(self, m, v, t: int, stream=None) -> None:
         """Continue after step t with these flat float32 moments (8-bit states: rounded). Their
         places behind a tensor may hold anything."""
         import torch
@@ -210,25 +239,34 @@ class AdamW:
         host[0] = t
         host[2:4] = torch.tensor([1.0 - self.beta1 ** t, 1.0 - self.beta2 ** t],
                                  dtype=torch.float64).view(torch.int64)
-        if self.eight:
-            onebit_adamw8_set_state(*self._state(), self._encodable(m), self._encodable(v))
-        else:
-            self.m.copy_(m.view(-1)[:self.total])
-            self.v.copy_(v.view(-1)[:self.total])
-        self.ctl.copy_(host)                     # last: a call that is refused changes nothing
+        with self._on(stream, (m, v)):
+            if self.eight:
+                onebit_adamw8_set_state(*self._state(), self._encodable(m), self._encodable(v))
+            else:
+                self.m.copy_(m.view(-1)[:self.total])
+                self.v.copy_(v.view(-1)[:self.total])
+            self.ctl.copy_(host)                 # last: a call that is refused changes nothing
 
-    def checkpoint(self) -> dict:
+    def _names(self):
+        return ("m", "v", "ctl") + (("m_exp", "v_exp") if self.eight else ())
+
+    def checkpoint(self, stream=None) -> dict:
         """Copies of everything a fresh AdamW of the same list needs to continue bit for bit."""
-        names = ("m", "v", "ctl") + (("m_exp", "v_exp") if self.eight else ())
-        return {n: getattr(self, n).clone() for n in names}
+        with self._on(stream) as current:
+            ck = {n: getattr(self, n).clone() for n in self._names()}
+        for x in ck.values():
+            if x.numel() > 0:
+                x.record_stream(current)
+        return ck
 
-    def restore(self, ck: dict) -> None:
-        names = ("m", "v", "ctl") + (("m_exp", "v_exp") if self.eight else ())
+    def restore(self, ck: dict, stream=None) -> None:
+        names = self._names()
         if set(ck) != set(names):
             raise ValueError("a checkpoint of another kind of state")
         for n in names:
             own = getattr(self, n)
             if ck[n].dtype != own.dtype or ck[n].shape != own.shape:
                 raise ValueError("checkpoint %s has another size or type" % n)
-        for n in names:
-            getattr(self, n).copy_(ck[n])
+        with self._on(stream, ck.values()):
+            for n in names:
+                getattr(self, n).copy_(ck[n])

@@ -68,3 +68,80 @@ def test_results_may_be_dropped_while_the_current_stream_reads_them(by):
     want = list(ob.onebit_adamw8_get_state(*state)) + list(ob.onebit_grad_norm(grads, 1.0))
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(copies, want)) and junk
+
+
+def busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(PAUSE)
+
+
+@pytest.mark.parametrize("by", ["stream", "handle"])
+@pytest.mark.parametrize("state", ["q8", "f32"])
+def test_everything_of_an_optimizer_on_one_other_stream(state, by):
+    """A clipped step, a checkpoint, another step, its moments, the checkpoint restored and the moments
+    set, all queued on a stream that is busy for some milliseconds, with no wait between the calls and
+    the inputs dropped at once: what they give is what the same calls on the current stream give."""
+    sizes = [70_001, 300, 0, 1 << 18]
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    start = [torch.randn(n, device=DEV, generator=gen) for n in sizes]
+    draws = [[torch.randn(n, device=DEV, generator=gen) for n in sizes] for _ in range(3)]
+
+    def run(side):
+        stream = side if by == "stream" or side is None else side.cuda_stream
+        p = [x.clone() for x in start]
+        opt = ob.AdamW(p, weight_decay=0.01, max_norm=1.0, state=state, seed=9)
+        given = torch.rand(2, opt.total, device=DEV, generator=torch.Generator(DEV).manual_seed(8))
+        grads = [[x.clone() for x in g] for g in draws]
+        out = []
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream())
+            busy(side)
+        opt.step(p, grads.pop(0), 1e-2, stream=stream)
+        ck = opt.checkpoint(stream=stream)
+        opt.step(p, grads.pop(0), 1e-2, stream=stream)
+        m, v = opt.get_state(stream=stream)
+        if side is not None:
+            with torch.cuda.stream(side):                 # 32-bit states: they are the states
+                out += [m.clone(), v.clone()]
+        else:
+            out += [m.clone(), v.clone()]
+        opt.restore(ck, stream=stream)
+        opt.step(p, grads.pop(0), 1e-2, stream=stream)
+        after = opt.checkpoint(stream=stream)
+        opt.set_state(given[0], given[1], 40, stream=stream)
+        del given, m, v
+        if side is not None:
+            junk = [torch.full((opt.total,), math.nan, device=DEV) for _ in range(4)]
+            assert junk
+        assert opt.counts() == (40, 0)
+        out += [ck[n] for n in sorted(ck)] + [after[n] for n in sorted(after)] + p
+        out += [*opt._state(), opt.ctl, opt.norm]
+        torch.cuda.synchronize()
+        return out
+    want, got = run(None), run(torch.cuda.Stream())
+    assert len(want) == len(got)
+    for i, (x, y) in enumerate(zip(got, want)):
+        assert torch.equal(x.reshape(-1).view(torch.uint8), y.reshape(-1).view(torch.uint8)), i
+
+
+def test_counts_waits_for_the_device():
+    p, g = [torch.zeros(1000, device=DEV)], [torch.ones(1000, device=DEV)]
+    opt = ob.AdamW(p)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    busy(side)
+    opt.step(p, g, 1e-3, stream=side)
+    assert opt.counts() == (1, 0)
+
+
+def test_a_checkpoint_is_the_memory_of_its_stream():
+    p = [torch.zeros(1 << 20, device=DEV)]
+    opt = ob.AdamW(p)
+    opt.m.fill_(3.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kept, copies = delayed_copies(1 << 20, torch.float32)
+    ck = opt.checkpoint(stream=side)
+    side.synchronize()
+    assert torch.equal(ck["m"].cpu(), torch.full((1 << 20,), 3.0))
+    assert all(torch.equal(x.cpu(), y) for x, y in zip(copies, kept))
