@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import operator
 from typing import List, Sequence, Tuple
 
 from . import _abi
@@ -251,22 +252,32 @@ class AdamW:
         return ("m", "v", "ctl") + (("m_exp", "v_exp") if self.eight else ())
 
     def checkpoint(self, stream=None) -> dict:
-        """Copies of everything a fresh AdamW of the same list needs to continue bit for bit."""
+        """Copies of everything a fresh AdamW of the same list and hyperparameters needs to continue
+        bit for bit: states and step count and, of 8-bit states, the seed of the rounding (a CPU
+        tensor, so that the whole can be saved or moved like the rest)."""
+        import torch
         with self._on(stream) as current:
             ck = {n: getattr(self, n).clone() for n in self._names()}
         for x in ck.values():
             if x.numel() > 0:
                 x.record_stream(current)
+        if self.eight:
+            bits = operator.index(self.seed) & (1 << 64) - 1
+            ck["seed"] = torch.tensor(bits - (bits >> 63 << 64), dtype=torch.int64)
         return ck
 
     def restore(self, ck: dict, stream=None) -> None:
+        """Continue from a checkpoint, with its seed (8-bit states; one without a seed leaves the
+        optimizer's own). A step that was captured before keeps the seed it was captured with."""
         names = self._names()
-        if set(ck) != set(names):
+        if set(ck) - ({"seed"} if self.eight else set()) != set(names):
             raise ValueError("a checkpoint of another kind of state")
         for n in names:
             own = getattr(self, n)
             if ck[n].dtype != own.dtype or ck[n].shape != own.shape:
                 raise ValueError("checkpoint %s has another size or type" % n)
-        with self._on(stream, ck.values()):
+        seed = int(ck["seed"]) if "seed" in ck else self.seed
+        with self._on(stream, [ck[n] for n in names]):
             for n in names:
                 getattr(self, n).copy_(ck[n])
+        self.seed = seed

@@ -153,3 +153,34 @@ def test_a_refused_clipped_step_changes_nothing(state, side):
     refused("overlap", work=arena[2 * n - 64:2 * n + 4032].view(torch.uint8))
     opt.step(p, other, 1e-2)
     assert float(opt.norm) == pytest.approx(2 * norm, rel=1e-6) and opt.counts() == (2, 0)
+
+
+@pytest.mark.parametrize("seed", [5, -1, (1 << 63) + 12345, (1 << 64) + 7])
+def test_a_checkpoint_continues_bit_for_bit_whatever_the_other_seed(seed, tmp_path):
+    """8-bit states: the rounding's seed is part of a checkpoint, saved and loaded like the rest; one
+    without it (or of 32-bit states, which round nothing at random) leaves the optimizer's own."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    grads = [[torch.randn(n, device=DEV, generator=gen) for n in SIZES] for _ in range(4)]
+    p = params()
+    opt = ob.AdamW(p, state="q8", seed=seed)
+    opt.step(p, grads[0], 1e-2)
+    opt.step(p, grads[1], 1e-2)
+    torch.save(opt.checkpoint(), tmp_path / "ck.pt")
+    q = [x.clone() for x in p]
+    other = ob.AdamW(q, state="q8", seed=99)
+    other.restore(torch.load(tmp_path / "ck.pt"))
+    for g in grads[2:]:
+        opt.step(p, g, 1e-2)
+        other.step(q, g, 1e-2)
+    for x, y in zip((*p, *opt._state(), opt.ctl), (*q, *other._state(), other.ctl)):
+        assert torch.equal(x, y)
+    ck = opt.checkpoint()
+    assert {k: v.cpu() for k, v in ck.items()}.keys() == ck.keys()
+    del ck["seed"]
+    third = ob.AdamW(q, state="q8", seed=42)
+    third.restore(ck)
+    assert third.seed == 42 and third.counts() == (4, 0)
+    narrow = ob.AdamW(q, state="f32", seed=42)
+    assert "seed" not in narrow.checkpoint()
+    with pytest.raises(ValueError, match="another kind"):
+        narrow.restore(opt.checkpoint())
