@@ -58,15 +58,13 @@ def _refuse(rc: int, where: str) -> None:
         raise _ob().OneBitError(rc, where, reason=True)
 
 
-def _int64s(values):
-    return (ctypes.c_int64 * len(values))(*values)
-
-
 def onebit_adamw_layout(numel: Sequence[int]) -> Tuple[List[int], int]:
     """Where each tensor's part of the flat states begins, and their whole length, in elements."""
     n = len(numel)
+    # ctypes would keep the lower 64 bits of a larger number
+    lengths = (ctypes.c_int64 * n)(*[x if -1 <= x < 1 << 63 else -1 for x in numel])
     offsets, total = (ctypes.c_int64 * n)(), ctypes.c_int64()
-    _refuse(_abi.lib().onebit_adamw_layout(n, _int64s(list(numel)), offsets, ctypes.byref(total)),
+    _refuse(_abi.lib().onebit_adamw_layout(n, lengths, offsets, ctypes.byref(total)),
             "onebit_adamw_layout")
     return list(offsets), total.value
 
