@@ -141,6 +141,10 @@ class AdamW:
         params = list(params)
         if not params:
             raise ValueError("no parameters")
+        if not isinstance(params[0], torch.Tensor):
+            raise TypeError("params must be a list of tensors")
+        if params[0].dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("params must be float32 or bfloat16, got %s" % params[0].dtype)
         for p in params:
             _ob()._device_vector(p, params[0].dtype, 0, "a parameter", params[0].device)
         self.lengths, self.device = [p.numel() for p in params], params[0].device
