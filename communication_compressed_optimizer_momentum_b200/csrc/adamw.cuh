@@ -181,12 +181,14 @@ unsigned grid_for(uint32_t nblk, int per_sm) {
                                        kSms * per_sm);
 }
 
-// No C++ exception leaves a C entry point: the lists are the only thing that allocates.
+// No C++ exception leaves a C entry point: the lists are the only thing that allocates. The reason
+// is short enough to need no memory itself.
 template <typename F>
 int guarded(F&& f) {
     try {
         return f();
     } catch (...) {
+        g_last_error = "no host memory";
         return ONEBIT_ERR_SPACE;
     }
 }

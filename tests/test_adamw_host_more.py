@@ -1,8 +1,15 @@
-"""More of AdamW without a GPU: lengths beyond 64 bits, and parameters that no step would take."""
+"""More of AdamW without a GPU: lengths beyond 64 bits, parameters that no step would take, and a
+host without memory."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import communication_compressed_optimizer_momentum_b200 as ob
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("n", [1 << 63, (1 << 64) - 1, 1 << 64, (1 << 64) + 300, -(1 << 63) - 1,
@@ -19,3 +26,29 @@ def test_an_optimizer_refuses_parameters_that_its_step_would(dtype, state):
         ob.AdamW([torch.zeros(8, dtype=dtype)], state=state)
     with pytest.raises(TypeError, match="list of tensors"):
         ob.AdamW([1.0], state=state)
+
+
+# 30 million empty tensors: their address ranges need 720 MB where 100 MB are left. Nothing is queued.
+NO_MEMORY = r"""
+import ctypes, resource, sys
+sys.path.insert(0, %r)
+import numpy as np
+from communication_compressed_optimizer_momentum_b200 import _abi
+L = _abi.lib()
+n = 30_000_000
+held = np.zeros(n, dtype=np.int64)
+zeros = held.ctypes.data
+assert L.onebit_grad_norm(1, zeros, zeros, 0, -1.0, 0, None, None) == -1
+assert b"max_norm" in L.onebit_last_error()
+size = [int(x.split()[1]) * 1024 for x in open("/proc/self/status") if x.startswith("VmSize")][0]
+resource.setrlimit(resource.RLIMIT_AS, (size + 100_000_000, resource.RLIM_INFINITY))
+rc = L.onebit_grad_norm(n, zeros, zeros, 0, 1.0, 0, 0x100000, None)
+print(rc, L.onebit_last_error().decode())
+""" % ROOT
+
+
+def test_a_host_without_memory_gives_its_own_reason():
+    """Not the reason of the call before; no exception leaves the C entry point."""
+    r = subprocess.run([sys.executable, "-c", NO_MEMORY], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split(None, 1) == ["-5", "no host memory\n"], \
+        r.stdout + r.stderr
