@@ -1,6 +1,8 @@
 """Build step for the CUDA library: compiles ``csrc/onebit_adam.cu`` for sm_100a into
 ``libonebit_adam.so`` next to this file (in-tree, so the built library travels with the repo), and
-``csrc/binding.cpp``, the binding's native part for lists of tensors, into ``_binding.so``.
+``csrc/binding.cpp``, the binding's native part for lists of tensors, into ``_binding.so``. The
+library needs neither torch nor Python's headers; the binding's part is left out where they are
+missing, and the functions that need it then raise.
 
 Run ``python -m communication_compressed_optimizer_momentum_b200.build`` or call ``build()``.
 """
@@ -49,11 +51,16 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library (and the binding's native part) if it is missing or older than its
-    sources; return the library's path."""
-    build_binding(force)
-    if not force and not stale():
-        return LIB
+    """Compile the library (and the binding's native part, where it can be) if it is missing or older
+    than its sources; return the library's path."""
+    if force or stale():
+        build_library(verbose)
+    if can_build_binding():
+        build_binding(force)
+    return LIB
+
+
+def build_library(verbose: bool = False) -> None:
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", SRC_DIR, "-o", tmp, *SOURCES]
     if verbose:
@@ -61,7 +68,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
-    return LIB
+
+
+def can_build_binding() -> bool:
+    """Whether torch and Python's headers are there."""
+    import importlib.util
+    import sysconfig
+    return importlib.util.find_spec("torch") is not None and \
+        os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
 
 
 def build_binding(force: bool = False) -> str:

@@ -1,5 +1,5 @@
-"""More of AdamW without a GPU: lengths beyond 64 bits, parameters that no step would take, and a
-host without memory."""
+"""More of AdamW without a GPU: lengths beyond 64 bits, parameters that no step would take, a
+host without memory, and what is built where."""
 import os
 import subprocess
 import sys
@@ -52,3 +52,40 @@ def test_a_host_without_memory_gives_its_own_reason():
     r = subprocess.run([sys.executable, "-c", NO_MEMORY], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split(None, 1) == ["-5", "no host memory\n"], \
         r.stdout + r.stderr
+
+
+# build.py by itself, as a program without torch or Python's headers uses it; the compilers' commands
+# are recorded, not run.
+BUILD = r"""
+import importlib.util, subprocess, sys, sysconfig
+missing, pkg = sys.argv[1], sys.argv[2]
+spec = importlib.util.spec_from_file_location("build_alone", pkg + "/build.py")
+build = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(build)
+if missing == "torch":
+    class NoTorch:
+        def find_spec(self, name, path=None, target=None):
+            if name.split(".")[0] == "torch":
+                raise ModuleNotFoundError(name)
+    sys.meta_path.insert(0, NoTorch())
+    find = importlib.util.find_spec
+    importlib.util.find_spec = lambda name, *a: None if name == "torch" else find(name, *a)
+elif missing == "headers":
+    paths = sysconfig.get_paths()
+    sysconfig.get_paths = lambda *a, **k: dict(paths, include="/nonexistent")
+ran = []
+build.subprocess.check_call = lambda cmd, **k: ran.append(cmd[0].split("/")[-1])
+build.os.replace = lambda a, b: ran.append("-> " + b.split("/")[-1])
+assert build.build(force=True) == build.LIB
+print(ran)
+"""
+
+
+@pytest.mark.parametrize("missing,want", [
+    ("torch", ["nvcc", "-> libonebit_adam.so"]), ("headers", ["nvcc", "-> libonebit_adam.so"]),
+    ("nothing", ["nvcc", "-> libonebit_adam.so", "g++", "-> _binding.so"])])
+def test_the_library_is_built_without_torch(missing, want):
+    pkg = os.path.join(ROOT, "communication_compressed_optimizer_momentum_b200")
+    r = subprocess.run([sys.executable, "-c", BUILD, missing, pkg], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == repr(want), r.stdout + r.stderr
