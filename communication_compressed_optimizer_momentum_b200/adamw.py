@@ -15,6 +15,7 @@ import contextlib
 import ctypes
 import math
 import operator
+import os
 from typing import List, Sequence, Tuple
 
 from . import _abi
@@ -31,14 +32,15 @@ def _binding():
     global _native
     if _native is None:
         L = _abi.lib()
+        import torch  # noqa: F401  (its libraries first)
+        again = "`python -m communication_compressed_optimizer_momentum_b200.build`"
+        if not os.path.exists(os.path.join(os.path.dirname(__file__), "_binding.so")):
+            raise RuntimeError("_binding.so is not built; run " + again)
         try:
-            import torch  # noqa: F401  (its libraries first)
-
             from . import _binding as native
         except ImportError as e:
-            raise RuntimeError(
-                "_binding.so is not built (%s); run "
-                "`python -m communication_compressed_optimizer_momentum_b200.build`" % e)
+            raise RuntimeError("_binding.so cannot be loaded (%s); if it is of another Python or "
+                               "torch, run %s" % (e, again)) from e
         names = ("onebit_adamw_step", "onebit_adamw8_step", "onebit_adamw8_get_state",
                  "onebit_adamw8_set_state", "onebit_grad_norm",
                  "onebit_internal_adamw_clipped_step")

@@ -35,6 +35,7 @@ NVCC_FLAGS = [
 
 
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = BINDING + ".stamp"
 BINDING_SOURCE = os.path.join(SRC_DIR, "binding.cpp")
 
 
@@ -78,29 +79,53 @@ def can_build_binding() -> bool:
         os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the binding's native part if it is missing or older than its sources."""
-    deps = (BINDING_SOURCE, os.path.join(SRC_DIR, "adamw_clip.h"),
-            os.path.join(INCLUDE, "onebit_adam.h"))
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(BINDING) >= os.path.getmtime(p) for p in deps):
-        return BINDING
+def binding_command(out: str) -> list:
     import sysconfig
 
     import torch
-    root = os.path.join(os.path.dirname(torch.__file__))
+    root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
-    tmp = BINDING + ".tmp%d" % os.getpid()
     includes = [INCLUDE, os.path.join(root, "include"),
                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     lib = os.path.join(root, "lib")
-    subprocess.check_call(
-        ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-         "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
-         *["-I" + p for p in includes], "-o", tmp, BINDING_SOURCE, "-L" + lib,
-         "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
-    os.replace(tmp, BINDING)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+            *["-I" + p for p in includes], "-o", out, BINDING_SOURCE, "-L" + lib,
+            "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def binding_stamp() -> str:
+    """What the native part is good for: the Python, the torch and the command it was built with
+    (wherever the tree lies: it may be moved)."""
+    import torch
+    command = " ".join(binding_command("_binding.so")).replace(ROOT + os.sep, "")
+    return "\n".join([sys.implementation.cache_tag, torch.__version__, command]) + "\n"
+
+
+def binding_stale() -> bool:
+    """Missing, older than its sources, or of another Python, torch or command."""
+    deps = (BINDING_SOURCE, os.path.join(SRC_DIR, "adamw_clip.h"),
+            os.path.join(INCLUDE, "onebit_adam.h"))
+    if not os.path.exists(BINDING) or \
+            any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps):
+        return True
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read() != binding_stamp()
+    except OSError:
+        return True
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the binding's native part if it is stale."""
+    if force or binding_stale():
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        subprocess.check_call(binding_command(tmp))
+        os.replace(tmp, BINDING)
+        with open(BINDING_STAMP + ".tmp%d" % os.getpid(), "w") as f:
+            f.write(binding_stamp())
+        os.replace(f.name, BINDING_STAMP)
     return BINDING
 
 

@@ -57,7 +57,7 @@ def test_a_host_without_memory_gives_its_own_reason():
 # build.py by itself, as a program without torch or Python's headers uses it; the compilers' commands
 # are recorded, not run.
 BUILD = r"""
-import importlib.util, subprocess, sys, sysconfig
+import importlib.util, os, subprocess, sys, sysconfig
 missing, pkg = sys.argv[1], sys.argv[2]
 spec = importlib.util.spec_from_file_location("build_alone", pkg + "/build.py")
 build = importlib.util.module_from_spec(spec)
@@ -75,7 +75,12 @@ elif missing == "headers":
     sysconfig.get_paths = lambda *a, **k: dict(paths, include="/nonexistent")
 ran = []
 build.subprocess.check_call = lambda cmd, **k: ran.append(cmd[0].split("/")[-1])
-build.os.replace = lambda a, b: ran.append("-> " + b.split("/")[-1])
+def replace(a, b):
+    if os.path.exists(a):                             # the note of what it was built with
+        os.remove(a)
+    else:
+        ran.append("-> " + b.split("/")[-1])
+build.os.replace = replace
 assert build.build(force=True) == build.LIB
 print(ran)
 """
@@ -89,3 +94,65 @@ def test_the_library_is_built_without_torch(missing, want):
     r = subprocess.run([sys.executable, "-c", BUILD, missing, pkg], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == repr(want), r.stdout + r.stderr
+
+
+def test_the_native_part_is_stale_with_another_torch_python_or_command(tmp_path, monkeypatch):
+    from communication_compressed_optimizer_momentum_b200 import build
+    build.build()
+    assert not build.binding_stale()                  # as it was built
+    built = tmp_path / "_binding.so"
+    built.write_bytes(b"")
+    monkeypatch.setattr(build, "BINDING", str(built))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(built) + ".stamp")
+    assert build.binding_stale()                      # nothing says what it was built with
+    commands = []
+    monkeypatch.setattr(build.subprocess, "check_call", lambda cmd: commands.append(cmd) or open(
+        cmd[cmd.index("-o") + 1], "w").close())
+    build.build_binding()
+    assert len(commands) == 1 and not build.binding_stale()
+    build.build_binding()
+    assert len(commands) == 1                         # nothing to do
+    with monkeypatch.context() as other:
+        other.setattr(torch, "__version__", "9.9")
+        assert build.binding_stale()
+    with monkeypatch.context() as other:
+        other.setattr(build, "nvcc", lambda: "/opt/other/cuda/bin/nvcc")
+        assert build.binding_stale()
+    assert not build.binding_stale()
+    with monkeypatch.context() as moved:              # the whole tree at another place
+        for name in ("ROOT", "PKG", "SRC_DIR", "INCLUDE", "BINDING_SOURCE"):
+            moved.setattr(build, name, getattr(build, name).replace(ROOT, "/else/where"))
+        stamp = build.binding_stamp()
+    assert stamp == build.binding_stamp() and ROOT not in stamp
+    monkeypatch.setattr(build.sys, "implementation", type("Other", (), {"cache_tag": "cpython-399"}))
+    assert build.binding_stale()
+    build.build_binding()
+    assert len(commands) == 2 and not build.binding_stale()
+
+
+UNLOADABLE = r"""
+import sys
+sys.path.insert(0, sys.argv[1])
+import communication_compressed_optimizer_momentum_b200 as ob
+import torch
+try:
+    ob.onebit_grad_norm([torch.zeros(3)])
+except RuntimeError as e:
+    print(e)
+"""
+
+
+@pytest.mark.parametrize("content,want", [(None, "not built"), (b"of another torch", "cannot be loaded")])
+def test_a_native_part_that_does_not_load_is_told_from_a_missing_one(tmp_path, content, want):
+    """In a copy of the package, whose _binding.so is missing or no library at all."""
+    name = "communication_compressed_optimizer_momentum_b200"
+    pkg = tmp_path / name
+    pkg.mkdir()
+    for f in os.listdir(os.path.join(ROOT, name)):
+        if f.endswith(".py") or f == "libonebit_adam.so":
+            os.symlink(os.path.join(ROOT, name, f), pkg / f)
+    if content is not None:
+        (pkg / "_binding.so").write_bytes(content)
+    r = subprocess.run([sys.executable, "-c", UNLOADABLE, str(tmp_path)], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "_binding.so " in r.stdout and want in r.stdout, r.stdout + r.stderr
