@@ -171,10 +171,10 @@ class Queue {
     // on with the result on the current stream: it is marked as used there.
     template <typename F>
     at::Tensor make(F&& allocate) const {
+        if (stream_.stream() == current_.stream()) return allocate();
         const c10::cuda::CUDAStreamGuard on(stream_);
         const at::Tensor t = allocate();
-        if (stream_.stream() != current_.stream() && t.numel() > 0)
-            t.record_stream(current_.unwrap());
+        if (t.numel() > 0) t.record_stream(current_.unwrap());
         return t;
     }
 
