@@ -74,7 +74,7 @@ def onebit_adamw_layout(numel: Sequence[int]) -> Tuple[List[int], int]:
 def onebit_adamw_step(params, grads, m, v, ctl, lr, beta1: float = 0.9, beta2: float = 0.999,
                       eps: float = 1e-8, weight_decay=0.0, copies=None, grad_scale=None,
                       bias_correction: bool = True, stream=None) -> None:
-    """One AdamW step over a list of tensors with fp32 states, in one launch.
+    """One AdamW step over a list of tensors with fp32 states, in one launch for up to 800 tensors.
 
     params, grads: lists of float32 or bfloat16 CUDA tensors (params and grads each of one type),
     any lengths, empty ones too. m, v: flat float32 states of ``onebit_adamw_layout``'s length.
@@ -116,7 +116,8 @@ def onebit_grad_norm(grads, max_norm: float = math.inf, work=None, accumulate: b
                      stream=None):
     """The l2 norm over a list of gradients and the factor that clips it to ``max_norm``: (norm,
     scale), float32 scalar tensors that stay on the device (views of ``work``; scale is a
-    ``grad_scale`` of the steps, NaN if the norm is not finite). work: uint8[16384], zeros before
+    ``grad_scale`` of the steps, NaN if the norm is not finite; the next call with the same work
+    overwrites both). work: uint8[16384], zeros before
     its first call; allocated if not given. accumulate: add to the sum of squares in ``work``, for a
     norm over several lists."""
     return _binding().grad_norm(grads, max_norm, work, accumulate, stream)
@@ -128,7 +129,7 @@ class AdamW:
 
     ``step(params, grads, lr)`` clips to ``max_norm`` if one is given (one launch for the norm; the
     norm, the factor and the skipping of a step whose norm is not finite stay on the device) and
-    updates every tensor in one launch. The parameters are the caller's; they are passed at every step.
+    updates the tensors in one launch for up to 800 of them. The parameters are the caller's; they are passed at every step.
 
     Every method that reads or writes the states takes a ``stream`` (default: the device's current
     one) and is ordered by it alone: a program that uses several streams makes each wait for the one
@@ -175,7 +176,8 @@ class AdamW:
 
     @property
     def norm(self):
-        """The last step's gradient norm before clipping (with max_norm), on the device."""
+        """The last step's gradient norm before clipping (with max_norm), on the device: a view that
+        the next step overwrites (``clone`` it to keep it)."""
         import torch
         return self.work[8:12].view(torch.float32)[0]
 

@@ -223,16 +223,19 @@ int queue_step(const TensorList& l, StepArgs a, cudaStream_t st) {
         a.advance = last ? 1 : 0;
         if constexpr (EIGHT) {
             const uint32_t units = (uint32_t)ceil_div(t.nblk + (t.blk0 & (kUnit - 1)), kUnit);
-            // fp32 parameters: shorter turns keep the streams closer together in memory (333.6M
-            // parameters with bf16 gradients and copies: 851 us against 872 with as many thread
-            // blocks as run at once); bf16 ones are bound by instructions (653 against 642).
+            // fp32 parameters: shorter turns keep the streams closer together in memory (with bf16
+            // gradients and copies, three times as many thread blocks as run at once against as
+            // many: 128M parameters 352 us / 360, 32M 92.4 / 95.9, 16M 48.3 / 48.8; below that they
+            // cost up to 5%, 5M 19.8 / 18.9, and up to 3M there are no more units than warps);
+            // bf16 ones are bound by instructions (32M 68.2 / 64.7, 8M 23.4 / 21.4).
             const int per_sm = sizeof(PT) == 4 ? 3 * kStepBlocks : kStepBlocks;
             launch(k_adamw8<PT, GT, N>, grid_for(units, per_sm), t, a, st);
         } else {
             // fp32 parameters: two thread blocks per SM keep the eight streams closer together in
-            // memory (333.6M parameters: 1394 us against 1509 with three, 103% of the measured
-            // copy bandwidth); bf16 ones need three for enough bytes in flight (1163 against
-            // 1274), and so do calls that end after a few blocks a warp.
+            // memory (all fp32, two against three: 333.6M parameters 1394 us / 1509, 32M 146 / 159,
+            // 8M 41.0 / 43.4, 5M 27.7 / 28.5); calls that end after a few blocks a warp want three
+            // (4M 23.1 / 23.1, 3M 18.9 / 18.3, 2M 14.7 / 13.7: equal at 16 blocks a warp, 4.85M).
+            // bf16 ones need three for enough bytes in flight (333.6M 1274 / 1163, 8M 37.6 / 33.8).
             const int per_sm =
                 sizeof(PT) == 4 && t.nblk >= (uint32_t)(kSms * kWarps * 16) ? 2 : kStepBlocks;
             launch(k_adamw<PT, GT, N>, grid_for(t.nblk, per_sm), t, a, st);

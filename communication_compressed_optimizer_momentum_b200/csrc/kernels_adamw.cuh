@@ -4,8 +4,8 @@
 // Work unit: a BLOCK of kBlk = 256 consecutive elements of one tensor, owned by one warp, eight
 // elements a lane. The states of all tensors lie in one flat vector in which every tensor begins
 // at a block boundary, so a block of a tensor is a block of the state. The tensors' addresses
-// travel in the kernel parameters (TensorTable, up to 30 KB), so a call queues exactly one launch
-// and keeps nothing: no table in device memory to upload, to go stale, or to be shared.
+// travel in the kernel parameters (TensorTable, up to 30 KB), so a call queues one launch for up to
+// 800 tensors and keeps nothing: no table in device memory to upload, to go stale, or to be shared.
 //
 // All of it streams HBM once; nothing is a contraction.
 #pragma once
@@ -327,7 +327,9 @@ k_adamw(const __grid_constant__ TensorTable<N> t, const StepArgs a) {
 //
 // Rounding in the step is stochastic: beta2 = 0.999 moves v by at most about 0.1 % a step, below
 // half a step of a 3-bit mantissa, so rounding to nearest would freeze v; rounding up with the
-// probability of the remainder keeps the mean of v (and m) that of the exact recurrence. A
+// probability of the remainder keeps the mean of v (and m) that of the exact recurrence, but for
+// what 16 random bits lose: 2^-17 of a spacing a rounding, v low by up to 2^-20 / (1 - beta2) of
+// itself (0.1 % at 0.999). A
 // positive v never gets code 0, so a denominator is at least 2^-16.5 of its block's largest, about
 // the ratio below which m reads as 0.
 
@@ -357,7 +359,8 @@ __device__ __forceinline__ void decode_factors(uint32_t k, float& f1, float& f2)
     f2 = k == kExpNan ? __int_as_float(0x7fffffff) : pow2(far);
 }
 
-// 32 random bits from 32: two rounds of xor-shift and odd multiplication.
+// 32 random bits from 32: two rounds of xor-shift and odd multiplication. Nothing but a test of the
+// bits' means and correlations speaks for the multipliers.
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x ^= x >> 16;
     x *= 0x9016D2F5u;
@@ -993,9 +996,9 @@ __device__ __forceinline__ double sumsq8(const T& raw, double acc) {
 
 // Units as in the 8-bit step: four loads in flight, and the walk over the tensors once for four
 // blocks. Bound by HBM: bf16, 665M elements: 202 us, 101% of the measured copy bandwidth (block by
-// block 270: the walk; a sustained loop at the power cap 230); fp32, 333.6M: 194 us, 105%. The blocks are counted from the address before a
-// tensor that takes vector loads, so that views at odd addresses are read as fast (333.6M element by
-// element: bf16 254 us, fp32 316).
+// block 270: the walk; a sustained loop at the power cap 230); fp32, 333.6M: 194 us, 105%. The
+// blocks are counted from the address before a tensor that takes vector loads, so that views at odd
+// addresses are read as fast (333.6M: bf16 119 us, fp32 195; element by element 254 and 316).
 template <typename GT, int N>
 __global__ void __launch_bounds__(kThreads, kNormPerSm)
 k_grad_norm(const __grid_constant__ TensorTable<N> t, const NormArgs a) {
