@@ -129,7 +129,8 @@ class AdamW:
 
     ``step(params, grads, lr)`` clips to ``max_norm`` if one is given (one launch for the norm; the
     norm, the factor and the skipping of a step whose norm is not finite stay on the device) and
-    updates the tensors in one launch for up to 800 of them. The parameters are the caller's; they are passed at every step.
+    updates the tensors in one launch for up to 800 of them. The parameters are the caller's; they are
+    passed at every step.
 
     Every method that reads or writes the states takes a ``stream`` (default: the device's current
     one) and is ordered by it alone: a program that uses several streams makes each wait for the one
@@ -193,8 +194,8 @@ class AdamW:
 
     @contextlib.contextmanager
     def _on(self, stream, given=()):
-        """``stream`` as the current one, and the states and the tensors given marked as used there;
-        yields the stream that was current."""
+        """``stream`` as the current one, nothing recorded for autograd, and the states and the
+        tensors given marked as used there; yields the stream that was current."""
         import torch
         current = torch.cuda.current_stream(self.device)
         if stream is None:
@@ -205,7 +206,7 @@ class AdamW:
         elif stream.device != self.device:
             raise ValueError("stream is on %s, the states are on %s" % (stream.device, self.device))
         try:
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(stream), torch.no_grad():
                 yield current
         finally:
             if stream != current:

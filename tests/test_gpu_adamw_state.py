@@ -184,3 +184,18 @@ def test_a_checkpoint_continues_bit_for_bit_whatever_the_other_seed(seed, tmp_pa
     assert "seed" not in narrow.checkpoint()
     with pytest.raises(ValueError, match="another kind"):
         narrow.restore(opt.checkpoint())
+
+
+@pytest.mark.parametrize("state", ["q8", "f32"])
+def test_moments_that_require_gradients_leave_states_that_do_not(state):
+    """A set_state is not part of anyone's graph."""
+    opt = ob.AdamW(params(), state=state)
+    m, v, _ = moments(opt, 7)
+    given = [torch.from_numpy(x).to(DEV).requires_grad_() for x in (m, v)]
+    opt.set_state(*given, 4)
+    assert not any(x.requires_grad for x in (*opt._state(), opt.ctl, *opt.get_state()))
+    ck = opt.checkpoint()
+    ck["m"] = ck["m"].float().requires_grad_().to(ck["m"].dtype)
+    other = ob.AdamW(params(), state=state)
+    other.restore(ck)
+    assert not any(x.requires_grad for x in (*other._state(), *other.checkpoint().values()))
