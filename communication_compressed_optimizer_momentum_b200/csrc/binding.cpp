@@ -278,7 +278,7 @@ void step(const char* where, const py::object& params, const py::object& grads,
 
     const Queue q(device, stream);
     int rc;
-    bool queued = false;   // a refusal queues nothing; what is queued uses its tensors even if it fails
+    bool queued = false;   // a refusal queues nothing; what is queued uses its tensors, come what may
     if (work.defined()) {
         OneBitAdamwClip a{};
         a.ntensors = p.n();

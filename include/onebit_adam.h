@@ -610,7 +610,8 @@ int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* param
 
 /*
  * The same step with states in 8 bits: m and v are codes (uint8[total], 16-byte aligned), m_exp
- * and v_exp one exponent k for each block of 256 elements (uint8[total / 256], 4-byte aligned). A code stands for
+ * and v_exp one exponent k for each block of 256 elements (uint8[total / 256], 4-byte aligned). A
+ * code stands for
  *   m: (-1)^(c>>7) * f(c & 127, 15) * 2^(k-127) ;   v: f(c, 31) * 2^(k-127)
  *   f(c, top) = c < 8 ? c/8 * 2^(1-top) : (1 + (c%8)/8) * 2^((c/8) - top)
  * and k = 255 makes the whole block NaN (it held an infinity, a NaN or a magnitude above
@@ -620,10 +621,10 @@ int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* param
  * probability of the remainder, in 16 bits), because a change of v by (1-beta2) of itself is far
  * below the spacing of 8-bit values and would be lost by rounding to nearest. 16 bits: a remainder
  * of r spacings is rounded up with probability floor(65536 r) / 65536, so that a rounding is low by
- * about 2^-17 of a spacing on average, which is at most 1/8 of the value. The means settle low by up
- * to 2^-20 / (1-beta) of themselves: m 0.001% at beta1 = 0.9; v 0.1% at beta2 = 0.999, 1% at 0.9999,
- * 10% at 0.99999 (from there on 32-bit states are the better choice). v > 0 never becomes
- * code 0. Where eps >= 2^-39 / sqrt(1 - beta2), which holds for every usual eps, the quotient
+ * about 2^-17 of a spacing on average; a spacing is at most 1/8 of a value whose code is not below
+ * 8. Such means settle low by up to 2^-20 / (1-beta) of themselves: m 0.001% at beta1 = 0.9; v 0.1%
+ * at beta2 = 0.999, 1% at 0.9999, 10% at 0.99999 (from there on 32-bit states are the better
+ * choice). v > 0 never becomes code 0. Where eps >= 2^-39 / sqrt(1 - beta2), which holds for every usual eps, the quotient
  * m / (...) comes from the hardware's approximate square root and reciprocal and a fused
  * multiply-add: within 2^-21 of itself, below the rounding of p; codes and exponents are exact.
  * The random bits are a function of seed, the step's number t (from 1) and the element's place i
@@ -632,9 +633,9 @@ int onebit_adamw_step(int32_t ntensors, const int64_t* numel, void* const* param
  *   key = mix(mix(mix(lo(seed) + G) ^ hi(seed)) + lo(t)) ;  G = 0x9E3779B9
  *   w = mix(lo(i/8) + key + hi(i/8) * G) ;  x = w + (i%8 + 1) * G
  *   x ^= x>>15, x *= 0x8A8866C7, x ^= x>>16 ;  16 bits for m: x>>16, for v: x & 0xffff
- * G is 2^32 divided by the golden ratio. No derivation stands behind the three odd multipliers: what is
- * asked of the bits (means, and correlations between places, steps, seeds and the two halves) is
- * tested.
+ * G is 2^32 divided by the golden ratio. No derivation stands behind the three odd multipliers:
+ * what is asked of the bits (means, and correlations between places, steps, seeds and the two
+ * halves) is tested.
  */
 int onebit_adamw8_step(int32_t ntensors, const int64_t* numel, void* const* params,
                        int32_t param_dtype, const void* const* grads, int32_t grad_dtype,
@@ -660,13 +661,14 @@ int onebit_adamw8_set_state(int64_t total, uint8_t* m, uint8_t* v, uint8_t* m_ex
                             const float* m_in, const float* v_in, void* stream);
 
 /*
- * The l2 norm over all gradients of a list (fp64 sums of squares, in an order that the lengths and the
- * addresses modulo 32 fix) and the factor that clips it: work (device, ONEBIT_GRAD_NORM_BYTES, 8-byte aligned, zero-filled before its first
- * call) receives double sum of squares, float norm, float scale = min(1, max_norm / norm), or NaN
- * if the norm is not finite. max_norm > 0, infinity for no clipping. accumulate = 1 adds to the sum
- * of squares that work holds: several lists of different types (or a sum reduced over ranks) make
- * one norm. The next call with the same work overwrites what it holds. scale's address (work + 12) is a grad_scale of the steps above. One call at a time may
- * use one work.
+ * The l2 norm over all gradients of a list (fp64 sums of squares, in an order that the lengths and
+ * the addresses modulo 32 fix) and the factor that clips it: work (device, ONEBIT_GRAD_NORM_BYTES,
+ * 8-byte aligned, zero-filled before its first call) receives double sum of squares, float norm,
+ * float scale = min(1, max_norm / norm), or NaN if the norm is not finite. max_norm > 0, infinity
+ * for no clipping. accumulate = 1 adds to the sum of squares that work holds: several lists of
+ * different types (or a sum reduced over ranks) make one norm. The next call with the same work
+ * overwrites what it holds. scale's address (work + 12) is a grad_scale of the steps above. One
+ * call at a time may use one work.
  */
 int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* grads,
                      int32_t grad_dtype, double max_norm, int32_t accumulate, void* work,
