@@ -43,7 +43,8 @@ def _binding():
                                "torch, run %s" % (e, again)) from e
         names = ("onebit_adamw_step", "onebit_adamw8_step", "onebit_adamw8_get_state",
                  "onebit_adamw8_set_state", "onebit_grad_norm",
-                 "onebit_internal_adamw_clipped_step")
+                 "onebit_internal_adamw_clipped_step", "onebit_mx4_layout", "onebit_mx4_quantize",
+                 "onebit_mx4_dequantize", "onebit_mx4_matmul")
         native.init({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names},
                     _ob().OneBitError)
         _native = native
@@ -168,7 +169,22 @@ class AdamW:
         self.ctl = zeros(CTL_BYTES // 8, torch.int64)
         self.work = zeros(NORM_BYTES, torch.uint8)
 
-    def step(self, params, grads, lr, copies=None, grad_scale=None, stream=None) -> None:
+    def step(self, params, grads, lr, copies=None, grad_scale=None, stream=None, mx4=None) -> None:
+        """One step. mx4: a list with an ``Mx4Linear`` or None for each parameter; their weights are
+        quantised again from the updated parameters, after the step and on its stream."""
+        if mx4 is not None:
+            params, mx4 = list(params), list(mx4)
+            if len(mx4) != len(params):
+                raise ValueError("%d mx4 entries for %d parameters" % (len(mx4), len(params)))
+            for p, linear in zip(params, mx4):
+                if linear is not None:
+                    linear.check_weight(p)
+        self._step(params, grads, lr, copies, grad_scale, stream)
+        for p, linear in zip(params, mx4 or ()):
+            if linear is not None:
+                linear.update(p, stream)
+
+    def _step(self, params, grads, lr, copies, grad_scale, stream) -> None:
         _binding().step(
             "onebit_adamw8_step" if self.eight else "onebit_adamw_step", params, grads,
             self._state(), self.ctl, lr, self.beta1, self.beta2, self.eps, self.weight_decay, copies,

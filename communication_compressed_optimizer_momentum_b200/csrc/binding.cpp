@@ -1,4 +1,4 @@
-// binding.cpp -- the native side of adamw.py: checks of tensors and lists of tensors, and the call
+// binding.cpp -- the native side of adamw.py and mx4.py: checks of tensors and lists of tensors, and the call
 // of the C entry points (whose addresses `init` is given, so that this module links to nothing of
 // the library's). A step over hundreds of tensors needs each one's type, device, layout, length
 // and address: about 1.1 us a tensor in Python, 20 ns here (a step over 240 small tensors: 272 us
@@ -27,6 +27,10 @@ decltype(&onebit_adamw8_get_state) p_get = nullptr;
 decltype(&onebit_adamw8_set_state) p_set = nullptr;
 decltype(&onebit_grad_norm) p_norm = nullptr;
 decltype(&onebit_internal_adamw_clipped_step) p_clipped = nullptr;
+decltype(&onebit_mx4_layout) p_mx4_layout = nullptr;
+decltype(&onebit_mx4_quantize) p_mx4_quantize = nullptr;
+decltype(&onebit_mx4_dequantize) p_mx4_dequantize = nullptr;
+decltype(&onebit_mx4_matmul) p_mx4_matmul = nullptr;
 PyObject* g_error = nullptr;  // OneBitError
 constexpr int kScaleOffset = 12;  // of the clip factor in the norm's work, in bytes
 
@@ -42,6 +46,10 @@ void init(const py::dict& addresses, const py::object& error) {
     address(p_set, addresses, "onebit_adamw8_set_state");
     address(p_norm, addresses, "onebit_grad_norm");
     address(p_clipped, addresses, "onebit_internal_adamw_clipped_step");
+    address(p_mx4_layout, addresses, "onebit_mx4_layout");
+    address(p_mx4_quantize, addresses, "onebit_mx4_quantize");
+    address(p_mx4_dequantize, addresses, "onebit_mx4_dequantize");
+    address(p_mx4_matmul, addresses, "onebit_mx4_matmul");
     g_error = error.inc_ref().ptr();
 }
 
@@ -429,6 +437,188 @@ py::tuple grad_norm(const py::object& grads, double max_norm, const py::object& 
     return py::make_tuple(both.select(0, 0), both.select(0, 1));
 }
 
+// ------------------------------------------------------------------------------------------
+// matrices in microscaled 4-bit floating point
+
+const at::Tensor& tensor(const py::handle& o, const std::string& name, const c10::Device* device) {
+    if (!THPVariable_Check(o.ptr())) throw py::type_error(name + " must be a torch.Tensor");
+    const at::Tensor& t = THPVariable_Unpack(o.ptr());
+    check_cuda(t, name, device);
+    return t;
+}
+
+// A plain matrix: two dimensions, consecutive columns, rows apart by its stride.
+const at::Tensor& plain(const py::handle& o, const std::string& name, const c10::Device* device) {
+    const at::Tensor& t = tensor(o, name, device);
+    if (t.dim() != 2)
+        throw py::value_error(name + " must have two dimensions, got " + std::to_string(t.dim()));
+    if (t.size(1) > 1 && t.stride(1) != 1)
+        throw py::value_error(name + " must have consecutive columns");
+    return t;
+}
+
+// A matrix in 4 bits: codes and exponents of its size.
+struct Packed {
+    at::Tensor codes, scales;
+    int64_t rows = 0, cols = 0;
+    uint8_t* c() const { return codes.defined() ? codes.data_ptr<uint8_t>() : nullptr; }
+    uint8_t* s() const { return scales.defined() ? scales.data_ptr<uint8_t>() : nullptr; }
+};
+
+void mx4_bytes(int64_t rows, int64_t cols, int64_t& codes, int64_t& scales) {
+    refuse(p_mx4_layout(rows, cols, &codes, &scales), "onebit_mx4_layout");
+}
+
+// From (codes, scales, rows, cols).
+Packed packed(const py::handle& o, const std::string& name, const c10::Device* device) {
+    const py::tuple t = py::cast<py::tuple>(o);
+    Packed p;
+    p.rows = py::cast<int64_t>(t[2]);
+    p.cols = py::cast<int64_t>(t[3]);
+    int64_t nc, ns;
+    mx4_bytes(p.rows, p.cols, nc, ns);
+    p.codes = vector(t[0], at::kByte, nc, name + ".codes", device);
+    const c10::Device d = p.codes.device();
+    p.scales = vector(t[1], at::kByte, ns, name + ".scales", &d);
+    return p;
+}
+
+Packed new_packed(const Queue& q, const at::Tensor& like, int64_t rows, int64_t cols) {
+    Packed p;
+    p.rows = rows;
+    p.cols = cols;
+    int64_t nc, ns;
+    mx4_bytes(rows, cols, nc, ns);
+    const auto opt = like.options().dtype(at::kByte).requires_grad(false);
+    p.codes = q.make([&] { return at::empty({rows, rows > 0 ? nc / rows : 0}, opt); });
+    p.scales = q.make([&] { return at::empty({ns}, opt); });
+    return p;
+}
+
+// out: None, or (codes, scales, rows, cols) of each form that is asked for, which are then written.
+// Returns (codes, scales, codes_t, scales_t), those of a form that is not asked for None.
+py::tuple mx4_quantize(const py::object& x_o, bool rows, bool columns, bool stochastic,
+                       const py::object& seed, const py::object& residual,
+                       const py::object& out_rows, const py::object& out_columns,
+                       const py::object& stream) {
+    const at::Tensor& x = plain(x_o, "x", nullptr);
+    const c10::Device device = x.device();
+    const int32_t code = dtype_code(x.scalar_type(), "x");
+    const int64_t r = x.size(0), c = x.size(1);
+    at::Tensor e;
+    if (!residual.is_none()) {
+        e = plain(residual, "residual", &device);
+        if (e.scalar_type() != at::kFloat)
+            throw py::type_error("residual must be torch.float32, got " + type_name(e.scalar_type()));
+        if (e.sizes() != x.sizes()) throw py::value_error("residual has another size than x");
+    }
+    Packed p[2];
+    const py::object* given[2] = {&out_rows, &out_columns};
+    const bool want[2] = {rows, columns};
+    for (int k = 0; k < 2; ++k) {
+        if (!want[k] || given[k]->is_none()) continue;
+        p[k] = packed(*given[k], "out", &device);
+        if (p[k].rows != (k ? c : r) || p[k].cols != (k ? r : c))
+            throw py::value_error("out is of another size");
+    }
+    const uint64_t key = PyLong_AsUnsignedLongLongMask(seed.ptr());
+    if (PyErr_Occurred()) throw py::error_already_set();
+    const Queue q(device, stream);
+    for (int k = 0; k < 2; ++k)
+        if (want[k] && !p[k].codes.defined()) p[k] = new_packed(q, x, k ? c : r, k ? r : c);
+    const int rc = p_mx4_quantize(
+        r, c, x.data_ptr(), code, x.stride(0), p[0].c(), p[0].s(), p[1].c(), p[1].s(),
+        stochastic ? 1 : 0, key, e.defined() ? e.data_ptr<float>() : nullptr,
+        e.defined() ? e.stride(0) : 0, q.handle());
+    if (rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA) {
+        q.uses(x);
+        q.uses(e);
+        for (const Packed& m : p) {
+            q.uses(m.codes);
+            q.uses(m.scales);
+        }
+        std::vector<const at::Tensor*> written;
+        if (e.defined()) written.push_back(&e);
+        for (const Packed& m : p)
+            if (m.codes.defined()) {
+                written.push_back(&m.codes);
+                written.push_back(&m.scales);
+            }
+        changed(written);
+    }
+    refuse(rc, "onebit_mx4_quantize");
+    const auto or_none = [](const at::Tensor& t) {
+        return t.defined() ? py::cast(t) : py::object(py::none());
+    };
+    return py::make_tuple(or_none(p[0].codes), or_none(p[0].scales), or_none(p[1].codes),
+                          or_none(p[1].scales));
+}
+
+at::ScalarType result_type(const py::object& dtype, const py::object& out, at::ScalarType other) {
+    if (!dtype.is_none()) {
+        if (!THPDtype_Check(dtype.ptr())) throw py::type_error("dtype must be a torch.dtype");
+        return reinterpret_cast<THPDtype*>(dtype.ptr())->scalar_type;
+    }
+    return THPVariable_Check(out.ptr()) ? THPVariable_Unpack(out.ptr()).scalar_type() : other;
+}
+
+// A result of a size and type: a given one, checked, or a new one.
+at::Tensor result(const py::object& out, const Queue& q, const at::Tensor& like, int64_t rows,
+                  int64_t cols, at::ScalarType type) {
+    const c10::Device device = like.device();
+    if (out.is_none())
+        return q.make([&] {
+            return at::empty({rows, cols}, like.options().dtype(type).requires_grad(false));
+        });
+    const at::Tensor& t = plain(out, "out", &device);
+    if (t.scalar_type() != type)
+        throw py::type_error("out must be " + type_name(type) + ", got " + type_name(t.scalar_type()));
+    if (t.size(0) != rows || t.size(1) != cols) throw py::value_error("out is of another size");
+    return t;
+}
+
+at::Tensor mx4_dequantize(const py::object& matrix, const py::object& dtype, const py::object& out,
+                          const py::object& stream) {
+    const Packed p = packed(matrix, "q", nullptr);
+    const at::ScalarType type = result_type(dtype, out, at::kFloat);
+    const int32_t code = dtype_code(type, "the values");
+    const Queue q(p.codes.device(), stream);
+    const at::Tensor t = result(out, q, p.codes, p.rows, p.cols, type);
+    const int rc = p_mx4_dequantize(p.rows, p.cols, p.c(), p.s(), t.data_ptr(), code, t.stride(0),
+                                    q.handle());
+    if (rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA) {
+        changed({&t});
+        q.uses(p.codes);
+        q.uses(p.scales);
+        q.uses(t);
+    }
+    refuse(rc, "onebit_mx4_dequantize");
+    return t;
+}
+
+at::Tensor mx4_matmul(const py::object& a_o, const py::object& b_o, const py::object& out,
+                      const py::object& dtype, bool accumulate, const py::object& stream) {
+    const Packed a = packed(a_o, "a", nullptr);
+    const c10::Device device = a.codes.device();
+    const Packed b = packed(b_o, "b", &device);
+    if (a.cols != b.cols)
+        throw py::value_error("a has " + std::to_string(a.cols) + " columns, b " +
+                              std::to_string(b.cols));
+    if (accumulate && out.is_none()) throw py::value_error("accumulate needs out");
+    const at::ScalarType type = result_type(dtype, out, at::kBFloat16);
+    const int32_t code = dtype_code(type, "out");
+    const Queue q(device, stream);
+    const at::Tensor t = result(out, q, a.codes, a.rows, b.rows, type);
+    const int rc = p_mx4_matmul(a.rows, b.rows, a.cols, a.c(), a.s(), b.c(), b.s(), t.data_ptr(),
+                                code, t.stride(0), accumulate ? 1 : 0, q.handle());
+    if (rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA) {
+        changed({&t});
+        for (const at::Tensor* x : {&a.codes, &a.scales, &b.codes, &b.scales, &t}) q.uses(*x);
+    }
+    refuse(rc, "onebit_mx4_matmul");
+    return t;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_binding, m) {
@@ -437,4 +627,7 @@ PYBIND11_MODULE(_binding, m) {
     m.def("get_state8", &get_state8);
     m.def("set_state8", &set_state8);
     m.def("grad_norm", &grad_norm);
+    m.def("mx4_quantize", &mx4_quantize);
+    m.def("mx4_dequantize", &mx4_dequantize);
+    m.def("mx4_matmul", &mx4_matmul);
 }

@@ -1,0 +1,735 @@
+// kernels_mx4.cuh -- matrices in microscaled 4-bit floating point for B200 (sm_100a): quantising,
+// reading back, and the product of two of them on the tensor cores.
+//
+// A matrix of rows x cols is held as codes (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6; two a byte, the even column in the lower half, rows of 16 * ceil(cols / 32) bytes) and
+// one power of two for each block of 32 consecutive columns of a row (a byte, the exponent plus 127;
+// 255: the whole block is NaN). The exponents lie in ATOMS of 128 rows by 4 blocks, 512 bytes: row r
+// and block b of an atom at (r % 32) * 16 + (r / 32) * 4 + b. That is the order in which the tensor
+// cores take them: one 32 x 128 bit copy from shared memory puts an atom into four columns of tensor
+// memory, and the two blocks of one 64-column instruction are the lower or the upper half of a word.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+#include "kernels_adamw.cuh"
+
+namespace onebit {
+
+constexpr int kMxBlk = 32;        // columns that share an exponent
+constexpr int kAtomRows = 128;    // of an atom of exponents
+constexpr int kAtomCols = 128;    // columns: four blocks
+constexpr int kAtomBytes = 512;
+constexpr int kMxNan = 255;
+
+__host__ __device__ inline int64_t mx4_blocks(int64_t cols) { return (cols + kMxBlk - 1) / kMxBlk; }
+__host__ __device__ inline int64_t mx4_pitch(int64_t cols) { return 16 * mx4_blocks(cols); }
+__host__ __device__ inline int64_t mx4_atoms(int64_t n) { return (n + kAtomCols - 1) / kAtomCols; }
+
+// Byte of the exponent of a row and a block within its atom.
+__device__ __forceinline__ int atom_at(int r, int b) { return (r & 31) * 16 + (r >> 5) * 4 + b; }
+
+// ------------------------------------------------------------------------------------------
+// quantising
+//
+// A block's exponent is the smallest with which its largest magnitude does not exceed 6:
+//   k = max(E - 2, 0), E the biased exponent of the largest magnitude, one more if its mantissa is
+//   above 1.5 (the sum with 0x3fffff carries then);  magnitudes above 1.5 * 2^127, infinities and NaN
+//   (E = 255) make the block NaN.
+// Nothing saturates, so that stochastic rounding has no bias. z = x * 2^(127 - k) is exact (a power
+// of two) unless it is below 2^-126, far below the smallest code's half.
+
+__device__ __forceinline__ uint32_t mx4_exponent(uint32_t most) {
+    const uint32_t e = (most + 0x3fffffu) >> 23;
+    return e >= 255u ? (uint32_t)kMxNan : (e > 2u ? e - 2u : 0u);
+}
+// 2^(127 - k), 0 for a NaN block (whose codes are then 0).
+__device__ __forceinline__ float mx4_inverse(uint32_t k) {
+    return k == kMxNan ? 0.0f : __uint_as_float((254u - k) << 23);
+}
+// 2^(k - 127), NaN for a NaN block.
+__device__ __forceinline__ float mx4_scale(uint32_t k) {
+    return k == kMxNan ? __uint_as_float(0x7fffffffu)
+                       : __uint_as_float(k > 0u ? k << 23 : 0x00400000u);
+}
+
+// Eight codes, rounded to nearest (ties to the even code): element i in bits 4i .. 4i + 3.
+__device__ __forceinline__ uint32_t encode8_nearest(const float (&z)[8]) {
+    uint32_t r;
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(r)
+        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+    return r;
+}
+
+// Eight codes, rounded up with the probability of the remainder in 16 bits. |z| * 2^-126 (rounded
+// toward zero: a remainder keeps 22 bits) lines the codes up with the upper bits of an fp32 pattern,
+// subnormal ones too; the random bits are added below them. |z| <= 6 cannot carry beyond the largest
+// code. w: the random word of the group of eight.
+__device__ __forceinline__ uint32_t encode8_stochastic(const float (&z)[8], uint32_t w) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        uint32_t x = w + (uint32_t)(p + 1) * kGolden;
+        x ^= x >> 15;
+        x *= 0x8A8866C7u;
+        x ^= x >> 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 2 * p + h;
+            const uint32_t y = __float_as_uint(__fmul_rz(fabsf(z[i]), 0x1p-126f));
+            const uint32_t add = h == 0 ? (x >> 16) << 6 : (x & 0xffffu) << 6;
+            r |= ((y + add) >> 22) << (4 * i);
+            r |= (__float_as_uint(z[i]) >> 31) << (4 * i + 3);
+        }
+    }
+    return r;
+}
+
+// The key of the random bits, and the word of the group of eight places that begins at place 8 G.
+__device__ __forceinline__ uint32_t mx4_key(uint64_t seed) {
+    return mix32(mix32((uint32_t)seed + kGolden) ^ (uint32_t)(seed >> 32));
+}
+
+template <bool SR>
+__device__ __forceinline__ uint32_t encode8(const float (&z)[8], uint32_t key, int64_t G) {
+    if constexpr (SR)
+        return encode8_stochastic(z, group_word(key, G));
+    else
+        return encode8_nearest(z);
+}
+
+// What eight codes stand for, but for the block's power of two.
+__device__ __forceinline__ void decode8(uint32_t c, float (&o)[8]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        uint32_t h;
+        asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n"
+            " cvt.rn.f16x2.e2m1x2 %0, a;\n}\n"
+            : "=r"(h)
+            : "r"(c >> (8 * p)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        o[2 * p] = f.x;
+        o[2 * p + 1] = f.y;
+    }
+}
+
+struct Mx4QuantArgs {
+    const void* x;
+    int64_t ld, rows, cols;
+    float* e;                  // residual (or null)
+    int64_t lde;
+    uint8_t *c, *s;            // the matrix: codes and exponents
+    uint8_t *ct, *st;          // the transposed matrix
+    uint64_t seed;             // of the matrix; the transposed one's is one more
+    int64_t col_tiles;
+    int32_t vec, vece;         // whole groups of eight are aligned for ld8
+};
+
+// Eight consecutive values from column `col` on, zeros behind the last.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t col, int64_t cols, bool vec,
+                                      float (&o)[8]) {
+    if (vec && col + 8 <= cols) {
+        ld8(row + col, o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = col + i < cols ? ld1(row + col + i) : 0.0f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void keep8(T* p, const float (&o)[8]);
+template <>
+__device__ __forceinline__ void keep8(float* p, const float (&o)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
+}
+template <>
+__device__ __forceinline__ void keep8(__nv_bfloat16* p, const float (&o)[8]) {
+    st8(p, o);
+}
+
+constexpr int kMxRows = 1, kMxColumns = 2;   // forms
+constexpr int kMxThreads = 256;
+
+template <typename T>
+__host__ __device__ constexpr int mx4_tile_bytes() {
+    return kAtomRows * kAtomCols * (int)sizeof(T);
+}
+template <typename T, int FORMS>
+__host__ __device__ constexpr int mx4_quant_smem() {
+    return (FORMS & kMxColumns) ? mx4_tile_bytes<T>() + kAtomRows * 64 + kAtomBytes : 0;
+}
+
+// A block of a column of the tile (32 rows from `rb` blocks on), eight at a time.
+template <bool SR>
+__device__ __forceinline__ uint4 encode_block(const float (&v)[32], uint32_t key, int64_t G,
+                                              uint32_t& k) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+    k = mx4_exponent(most);
+    const float inv = mx4_inverse(k);
+    uint32_t w[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = v[8 * g + i] * inv;
+        w[g] = k == kMxNan ? 0u : encode8<SR>(z, key, G + g);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One thread block takes ROWS x 128 values: of 128 rows, an atom of exponents in either form. Rows:
+// 16 lanes a row, eight columns a lane, four lanes a block. Columns: the values pass through shared
+// memory and a thread takes blocks of 32 rows; the codes go out through shared memory as well, so
+// that 64 bytes of a row of the transposed matrix are written together.
+template <typename T, int FORMS, bool SR, bool RES, int ROWS>
+__global__ void __launch_bounds__(kMxThreads) k_mx4_quantize(const Mx4QuantArgs a) {
+    static_assert(!(FORMS & kMxColumns) || ROWS == kAtomRows, "blocks of 32 rows");
+    static_assert(!RES || FORMS == kMxRows, "the residual is the rows' form's");
+    extern __shared__ __align__(128) uint8_t sm[];
+    T* tile = reinterpret_cast<T*>(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t ct = blockIdx.x % a.col_tiles, rt = blockIdx.x / a.col_tiles;
+    const int64_t r0 = rt * ROWS, c0 = ct * kAtomCols;
+    const T* x = static_cast<const T*>(a.x);
+    const int sub = lane >> 4, g = lane & 15;
+    const int64_t col = c0 + g * 8;
+    const int64_t pitch = mx4_pitch(a.cols);
+    const uint32_t key = SR ? mx4_key(a.seed) : 0u;
+    constexpr int kIter = ROWS / 16, kBatch = kIter < 4 ? kIter : 4;
+#pragma unroll 1
+    for (int it = 0; it < kIter; it += kBatch) {
+        float v[kBatch][8], e[RES ? kBatch : 1][8];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = (it + u) * 16 + warp * 2 + sub;
+            const int64_t row = r0 + r;
+            const bool in = row < a.rows;
+            load8(x + (in ? row * a.ld : 0), col, in ? a.cols : 0, a.vec, v[u]);
+            if constexpr (RES) load8(a.e + (in ? row * a.lde : 0), col, in ? a.cols : 0, a.vece, e[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = (it + u) * 16 + warp * 2 + sub;
+            const int64_t row = r0 + r;
+            if constexpr (FORMS & kMxColumns) keep8(tile + r * kAtomCols + g * 8, v[u]);
+            if constexpr (FORMS & kMxRows) {
+                if constexpr (RES) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[u][i] = __fadd_rn(v[u][i], e[u][i]);
+                }
+                uint32_t most = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    most = max(most, __float_as_uint(v[u][i]) & 0x7fffffffu);
+                most = max(most, __shfl_xor_sync(kFull, most, 1));
+                most = max(most, __shfl_xor_sync(kFull, most, 2));
+                const uint32_t k = mx4_exponent(most);
+                const float inv = mx4_inverse(k);
+                float z[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = v[u][i] * inv;
+                const uint32_t w = k == kMxNan ? 0u : encode8<SR>(z, key, (row * pitch + col / 2) / 4);
+                if (row < a.rows && col / 2 < pitch)
+                    *reinterpret_cast<uint32_t*>(a.c + row * pitch + col / 2) = w;
+                if ((g & 3) == 0)
+                    a.s[((row >> 7) * a.col_tiles + ct) * kAtomBytes + atom_at((int)(row & 127), g >> 2)] =
+                        (uint8_t)k;
+                if constexpr (RES) {
+                    float q[8];
+                    decode8(w, q);
+                    const float scale = mx4_scale(k);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] = __fsub_rn(v[u][i], q[i] * scale);
+                    if (row < a.rows) {
+                        float* er = a.e + row * a.lde;
+                        if (a.vece && col + 8 <= a.cols) {
+                            st8(er + col, q);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (col + i < a.cols) er[col + i] = q[i];
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if constexpr (FORMS & kMxColumns) {
+        uint8_t* codes = sm + mx4_tile_bytes<T>();        // [128 columns][4 blocks][16 bytes]
+        uint8_t* exps = codes + kAtomRows * 64;           // [128 columns][4 blocks]
+        const uint32_t tkey = SR ? mx4_key(a.seed + 1) : 0u;
+        const int64_t tpitch = mx4_pitch(a.rows);
+        const int64_t row_tiles = mx4_atoms(a.rows);
+        __syncthreads();
+        const auto put = [&](const float (&v)[32], int c, int b) {
+            uint32_t k;
+            const int64_t G = ((c0 + c) * tpitch + r0 / 2) / 4 + b * 4;
+            const uint4 w = encode_block<SR>(v, tkey, G, k);
+            *reinterpret_cast<uint4*>(codes + c * 64 + ((b ^ (c >> 1)) & 3) * 16) = w;
+            exps[c * 4 + b] = (uint8_t)k;
+        };
+        if constexpr (sizeof(T) == 4) {
+            const int c = tid & 127;
+#pragma unroll 1
+            for (int b = tid >> 7; b < 4; b += 2) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = reinterpret_cast<const float*>(tile)[(b * 32 + i) * 128 + c];
+                put(v, c, b);
+            }
+        } else {
+            const int c = (tid & 63) * 2, b = tid >> 6;
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                p[i] = reinterpret_cast<const uint32_t*>(tile)[(b * 32 + i) * 64 + (tid & 63)];
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(p[i] << 16);
+            put(v, c, b);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(p[i] & 0xffff0000u);
+            put(v, c + 1, b);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = tid; i < kAtomCols * 4; i += kMxThreads) {
+            const int c = i >> 2, b = i & 3;
+            const int64_t at = r0 / 2 + b * 16;
+            if (c0 + c < a.cols && at < tpitch)
+                *reinterpret_cast<uint4*>(a.ct + (c0 + c) * tpitch + at) =
+                    *reinterpret_cast<const uint4*>(codes + c * 64 + ((b ^ (c >> 1)) & 3) * 16);
+        }
+        if (tid < kAtomCols)
+            *reinterpret_cast<uint32_t*>(a.st + (ct * row_tiles + rt) * kAtomBytes + atom_at(tid, 0)) =
+                *reinterpret_cast<const uint32_t*>(exps + tid * 4);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// reading back
+
+struct Mx4DequantArgs {
+    const uint8_t *c, *s;
+    void* out;
+    int64_t ld, rows, cols, col_tiles;
+    int32_t vec;
+};
+
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize(const Mx4DequantArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t ct = blockIdx.x % a.col_tiles, rt = blockIdx.x / a.col_tiles;
+    const int g = lane & 15;
+    const int64_t col = ct * kAtomCols + g * 8, pitch = mx4_pitch(a.cols);
+    if (col >= a.cols) return;
+#pragma unroll
+    for (int it = 0; it < ROWS / 16; ++it) {
+        const int64_t row = rt * ROWS + it * 16 + warp * 2 + (lane >> 4);
+        if (row >= a.rows) continue;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.c + row * pitch + col / 2);
+        const float scale =
+            mx4_scale(a.s[((row >> 7) * a.col_tiles + ct) * kAtomBytes + atom_at((int)(row & 127), g >> 2)]);
+        float v[8];
+        decode8(w, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= scale;
+        T* out = static_cast<T*>(a.out) + row * a.ld + col;
+        if (a.vec && col + 8 <= a.cols) {
+            st8(out, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < a.cols) st1(out + i, v[i]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// the product: out[i][j] = sum_k a[i][k] b[j][k]
+//
+// One thread block takes 128 columns of out (rows of b) by TM rows of out (rows of a). b's rows are the
+// 128 lanes of the accumulator in tensor memory, so that a warp's stores of one row of out are
+// consecutive whatever its strides are, and so that few rows of a (one token) take a narrow
+// instruction rather than an empty one. A stage is 256 columns of both operands (128 bytes of a row,
+// one 128-byte swizzle atom) with their exponents, four instructions of 64 columns.
+//
+// Warps: 0 loads (TMA), 1 issues the copies of exponents and the products, 2 to 5 write out.
+
+constexpr int kMmThreads = 192;
+constexpr int kMmLanes = 128;             // rows of b in a tile
+constexpr int kStageCols = 256;
+constexpr uint32_t kMmTimeout = 1u;
+
+__device__ uint32_t g_mx4_status;
+
+template <int TM>
+struct MmTile {
+    static constexpr int kHalves = TM > 128 ? 2 : 1;          // atoms of a's exponents across
+    static constexpr int kB = kMmLanes * 128, kA = TM * 128;  // bytes of codes in a stage
+    static constexpr int kSB = 2 * kAtomBytes, kSA = 2 * kHalves * kAtomBytes;
+    static constexpr int kStage = kB + kA + kSB + kSA;
+    static constexpr int kStages = TM == 256 ? 4 : TM == 128 ? 6 : 8;
+    static constexpr int kSmem = kStages * kStage + 1024 + 256;  // alignment, barriers
+    // Tensor memory: two accumulators and the exponents. Two of 256 columns leave no room: they
+    // overlap by 32 columns, which are written out first.
+    static constexpr int kSecond = TM == 256 ? 224 : TM;
+    static constexpr int kExp = kSecond + TM;
+    static constexpr int kNeed = kExp + 8 + 8 * kHalves;
+    static constexpr int kColumns = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    static constexpr int kChunk = TM < 32 ? TM : 32;          // columns written out at a time
+};
+
+struct Mx4MatmulArgs {
+    const uint8_t *sa, *sb;
+    void* out;
+    int64_t ld;
+    int32_t m, n;              // rows and columns of out
+    int32_t steps;             // products of 64 columns
+    int32_t stages;            // of 256 columns
+    int32_t atoms;             // of exponents along the columns
+    int32_t tiles_m, tiles_n;
+    int32_t accumulate;
+};
+
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// The barrier completes when all copies and products issued so far by this thread are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_copy_atom(uint32_t column, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(column), "l"(desc)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t sa, uint32_t sb, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+}
+
+// Shared memory descriptors: rows of 128 bytes in 128-byte swizzle atoms of eight (1024 bytes apart),
+// and plain groups of eight 16-byte rows (128 bytes apart) for the exponents.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+__device__ __forceinline__ uint64_t atom_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
+}
+
+// Both operands 4-bit (E2M1), exponents as powers of two, 128 x TM, fp32 sums; half: which blocks of
+// the exponents' words.
+template <int TM>
+__device__ __forceinline__ uint32_t product_desc(uint32_t half) {
+    return (2 * half) << 4 | 1u << 7 | 1u << 10 | (uint32_t)(TM / 8) << 17 | 1u << 23 |
+           (uint32_t)(kMmLanes / 16) << 24 | (2 * half) << 29;
+}
+
+template <int N>
+__device__ __forceinline__ void tc_load(uint32_t addr, float (&v)[N]);
+template <>
+__device__ __forceinline__ void tc_load(uint32_t addr, float (&v)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void tc_load(uint32_t addr, float (&v)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// A float of another thread block of the cluster, at this block's address of it.
+__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+    uint32_t p;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+    return v;
+}
+
+template <typename OT>
+__device__ __forceinline__ void put_out(OT* p, float v, bool add) {
+    if constexpr (sizeof(OT) == 4) {
+        *p = add ? *p + v : v;
+    } else {
+        *p = __float2bfloat16_rn(v);
+    }
+}
+
+// SPLIT: a cluster of thread blocks shares one tile, each with a part of the common axis; their sums
+// are added in the blocks' order through shared memory. Otherwise a block walks over tiles, and the
+// products of one tile run while the last one is written out.
+template <int TM, typename OT, bool SPLIT>
+__global__ void __launch_bounds__(kMmThreads, 1)
+k_mx4_matmul(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const Mx4MatmulArgs p) {
+    using S = MmTile<TM>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* const sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    uint64_t* const full = reinterpret_cast<uint64_t*>(sm + S::kStages * S::kStage);
+    uint64_t* const empty = full + S::kStages;
+    uint64_t* const done = empty + S::kStages;      // [2] an accumulator is complete
+    uint64_t* const drained = done + 2;             // [2] ... and read as far as the next needs
+    uint64_t* const last = drained + 2;
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(last + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(done + i, 1);
+            mbar_init(drained + i, 4);
+        }
+        mbar_init(last, 1);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(tmem_at)),
+                     "r"(S::kColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    const int split = SPLIT ? (int)cluster_rank() : 0;
+    const int nsplit = SPLIT ? (int)(gridDim.x / (p.tiles_m * p.tiles_n)) : 1;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    const int64_t first = SPLIT ? blockIdx.x / nsplit : blockIdx.x;
+    const int64_t hop = SPLIT ? tiles : gridDim.x;
+    const int k0 = SPLIT ? (int)((int64_t)p.stages * split / nsplit) : 0;
+    const int k1 = SPLIT ? (int)((int64_t)p.stages * (split + 1) / nsplit) : p.stages;
+    // Bands of 16 tiles along b's rows, so that the tiles that run together share their operands in L2.
+    const auto place = [&](int64_t t, int& tm, int& tn) {
+        const int64_t band = t / (16ll * p.tiles_m);
+        const int wide = min(16, p.tiles_n - (int)band * 16);
+        const int r = (int)(t - band * 16 * p.tiles_m);
+        tm = r / wide;
+        tn = (int)band * 16 + r % wide;
+    };
+    bool ok = true;
+
+    if (warp == 0 && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t filled = 0;
+        for (int64_t t = first; t < tiles && ok; t += hop) {
+            int tm, tn;
+            place(t, tm, tn);
+            const int arow = tm * TM / kAtomRows;
+            const int atoms_a = min(S::kHalves, (int)mx4_atoms(p.m) - arow);
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = mbar_wait_bounded(empty + stage, phase ^ 1))) break;
+                uint8_t* s = sm + stage * S::kStage;
+                const int atoms = min(2, p.atoms - 2 * k) * kAtomBytes;
+                mbar_arrive_expect_tx(full + stage, S::kB + S::kA + atoms * (1 + atoms_a));
+                tma_tile(s, &map_b, k * 128, tn * kMmLanes, full + stage);
+                tma_tile(s + S::kB, &map_a, k * 128, tm * TM, full + stage);
+                bulk_load(s + S::kB + S::kA, p.sb + ((int64_t)tn * p.atoms + 2 * k) * kAtomBytes,
+                          atoms, full + stage);
+                for (int h = 0; h < atoms_a; ++h)
+                    bulk_load(s + S::kB + S::kA + S::kSB + h * 2 * kAtomBytes,
+                              p.sa + ((int64_t)(arow + h) * p.atoms + 2 * k) * kAtomBytes, atoms,
+                              full + stage);
+                ++filled;
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok) {  // leave no copy in flight behind
+            atomicOr(&g_mx4_status, kMmTimeout);
+            for (int64_t f = filled > S::kStages ? filled - S::kStages : 0; f < filled; ++f)
+                mbar_wait_bounded(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1);
+        }
+    } else if (warp == 1 && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t i = 0;
+        for (int64_t t = first; t < tiles && ok; t += hop, ++i) {
+            int tm, tn;
+            place(t, tm, tn);
+            // a's exponents: the tile's first row within its atom, in columns of 32 rows
+            const uint32_t sub = TM < kAtomRows ? (uint32_t)(tm * TM % kAtomRows) / 32 : 0u;
+            const uint32_t d = tmem + (uint32_t)(i & 1) * S::kSecond;
+            const int64_t before = TM == 256 ? i - 1 : i - 2;  // the tile that has to be read first
+            if (before >= 0 &&
+                !(ok = mbar_wait_bounded(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
+                break;
+            tc_fence_after();
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = mbar_wait_bounded(full + stage, phase))) break;
+                tc_fence_after();
+                const uint32_t s = smem_addr(sm + stage * S::kStage);
+                const int atoms = min(2, p.atoms - 2 * k), steps = min(4, p.steps - 4 * k);
+                const uint32_t eb = tmem + S::kExp, ea = eb + 8;
+                for (int c = 0; c < atoms; ++c) {
+                    tc_copy_atom(eb + 4 * c, atom_desc(s + S::kB + S::kA + c * kAtomBytes));
+#pragma unroll
+                    for (int h = 0; h < S::kHalves; ++h)
+                        tc_copy_atom(ea + 4 * (c * S::kHalves + h),
+                                     atom_desc(s + S::kB + S::kA + S::kSB + (2 * h + c) * kAtomBytes));
+                }
+                for (int q = 0; q < steps; ++q)
+                    tc_product(d, tile_desc(s) + 2 * q, tile_desc(s + S::kB) + 2 * q,
+                               product_desc<TM>(q & 1), eb + 4 * (q >> 1),
+                               ea + 4 * S::kHalves * (q >> 1) + sub, k > k0 || q > 0);
+                tc_commit(empty + stage);
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok) tc_commit(done + (i & 1));
+        }
+        if (!ok) {
+            atomicOr(&g_mx4_status, kMmTimeout);
+            tc_commit(last);
+            mbar_wait_bounded(last, 0);
+        }
+    } else if (warp >= 2) {
+        const int quad = warp & 3;
+        int64_t i = 0;
+        for (int64_t t = first; t < tiles && ok; t += hop, ++i) {
+            int tm, tn;
+            place(t, tm, tn);
+            const int buf = (int)(i & 1);
+            if (!(ok = mbar_wait_bounded(done + buf, (uint32_t)(i >> 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + buf * S::kSecond + ((uint32_t)(quad * 32) << 16);
+            const int64_t m0 = (int64_t)tm * TM;
+            const int n = tn * kMmLanes + quad * 32 + lane;
+            constexpr int kChunks = TM / S::kChunk;
+#pragma unroll 1
+            for (int u = 0; u < kChunks; ++u) {
+                // the columns that the other accumulator shares come first: the last of the first one,
+                // the first of the second
+                const int j0 = (TM == 256 && buf == 0 ? kChunks - 1 - u : u) * S::kChunk;
+                float v[S::kChunk];
+                __syncwarp();
+                tc_load(d + j0, v);
+                if (!SPLIT && u == (TM == 256 ? 0 : kChunks - 1)) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(drained + buf);
+                }
+                if constexpr (SPLIT) {
+                    float* part = reinterpret_cast<float*>(sm);
+#pragma unroll
+                    for (int j = 0; j < S::kChunk; ++j)
+                        part[(j0 + j) * kMmLanes + quad * 32 + lane] = v[j];
+                } else if (n < p.n) {
+                    OT* out = static_cast<OT*>(p.out) + (m0 + j0) * p.ld + n;
+                    const int rows = (int)min((int64_t)S::kChunk, p.m - m0 - j0);
+                    if (sizeof(OT) == 4 && p.accumulate) {
+                        float o[S::kChunk];
+#pragma unroll
+                        for (int j = 0; j < S::kChunk; ++j)
+                            o[j] = j < rows ? (float)out[j * p.ld] : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < S::kChunk; ++j) v[j] += o[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < S::kChunk; ++j)
+                        if (j < rows) st1(out + j * p.ld, v[j]);
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(&g_mx4_status, kMmTimeout);
+    }
+    __syncwarp();
+    if constexpr (SPLIT) {
+        cluster_sync();
+        int tm, tn;
+        place(first, tm, tn);
+        const int64_t m0 = (int64_t)tm * TM;
+        const int rows = (int)min((int64_t)TM, p.m - m0);
+        const int j1 = (int)((int64_t)rows * (split + 1) / nsplit);
+        for (int j = (int)((int64_t)rows * split / nsplit) + (int)threadIdx.x / 64; j < j1; j += 3) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int l = (int)(threadIdx.x & 63) + 64 * h, n = tn * kMmLanes + l;
+                const uint32_t at = smem_addr(sm) + (j * kMmLanes + l) * 4;
+                float v = cluster_load(at, 0);
+                for (int r = 1; r < nsplit; ++r) v += cluster_load(at, r);
+                if (n < p.n)
+                    put_out(static_cast<OT*>(p.out) + (m0 + j) * p.ld + n, v, p.accumulate != 0);
+            }
+        }
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(S::kColumns));
+}
+
+}  // namespace onebit

@@ -1,0 +1,336 @@
+// mx4.cuh -- host side of the entry points for matrices in microscaled 4-bit floating point
+// (onebit_mx4_*): argument checks, the choice of tiles and the launches. Included by onebit_adam.cu.
+#pragma once
+
+#include <atomic>
+
+#include "host.h"
+#include "kernels_mx4.cuh"
+
+namespace {
+
+constexpr int64_t kMxMost = (int64_t)1 << 30;  // rows or columns
+
+int64_t mx4_code_bytes(int64_t rows, int64_t cols) { return rows * mx4_pitch(cols); }
+int64_t mx4_scale_bytes(int64_t rows, int64_t cols) {
+    return mx4_atoms(rows) * mx4_atoms(cols) * kAtomBytes;
+}
+
+int mx4_shape(const char* where, int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0 || rows > kMxMost || cols > kMxMost) return bad(where, "bad size of a matrix");
+    return ONEBIT_OK;
+}
+
+// Codes and exponents of one matrix. Empty matrices have neither.
+int mx4_matrix(const char* where, int64_t rows, int64_t cols, const void* codes,
+               const void* scales) {
+    if (rows == 0 || cols == 0) return ONEBIT_OK;
+    if (codes == nullptr || scales == nullptr) return bad(where, "null codes or exponents");
+    if (!aligned16(codes) || !aligned16(scales))
+        return bad(where, "codes or exponents not 16-byte aligned", ONEBIT_ERR_ALIGN);
+    return ONEBIT_OK;
+}
+
+// A plain matrix with rows `ld` elements apart.
+int mx4_plain(const char* where, const char* what, int64_t rows, int64_t cols, const void* x,
+              int64_t ld, int64_t w) {
+    if (rows == 0 || cols == 0) return ONEBIT_OK;
+    if (x == nullptr) return bad(where, std::string("null ") + what);
+    if (!aligned_to(x, w))
+        return bad(where, std::string(what) + " not aligned to its elements", ONEBIT_ERR_ALIGN);
+    if (rows > 1 && (ld < cols || ld > ((int64_t)1 << 40)))
+        return bad(where, std::string("bad row stride of ") + what);
+    return ONEBIT_OK;
+}
+
+int64_t mx4_span(int64_t rows, int64_t cols, int64_t ld, int64_t w) {
+    return rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * w;
+}
+
+// Shared memory beyond 48 KB is asked for once for each kernel and device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+template <typename T, int FORMS, bool SR, bool RES, int ROWS>
+int launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t st) {
+    constexpr int smem = mx4_quant_smem<T, FORMS>();
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = k_mx4_quantize<T, FORMS, SR, RES, ROWS>;
+    if (smem > 48 * 1024) ONEBIT_CUDA(allow_smem(kernel, smem, done));
+    const int64_t blocks = a.col_tiles * mx4_atoms(a.rows) * (kAtomRows / ROWS);
+    kernel<<<(unsigned)blocks, kMxThreads, smem, st>>>(a);
+    ONEBIT_CUDA(cudaGetLastError());
+    return ONEBIT_OK;
+}
+
+template <typename T, bool SR>
+int queue_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t st) {
+    const bool rows = a.c != nullptr, columns = a.ct != nullptr;
+    if (rows && columns) return launch_mx4_quantize<T, kMxRows | kMxColumns, SR, false, 128>(a, st);
+    if (columns) return launch_mx4_quantize<T, kMxColumns, SR, false, 128>(a, st);
+    if (a.e != nullptr) return launch_mx4_quantize<T, kMxRows, SR, true, 32>(a, st);
+    return launch_mx4_quantize<T, kMxRows, SR, false, 32>(a, st);
+}
+
+// cuTensorMapEncodeTiled, asked of the runtime: the library links to no driver library.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int encode_tiled(EncodeTiled* f) {
+    static std::atomic<void*> found{nullptr};
+    void* p = found.load(std::memory_order_acquire);
+    if (p == nullptr) {
+        cudaDriverEntryPointQueryResult q;
+        ONEBIT_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q));
+        if (q != cudaDriverEntryPointSuccess || p == nullptr)
+            return cuda_fail(cudaErrorSymbolNotFound);
+        found.store(p, std::memory_order_release);
+    }
+    *f = reinterpret_cast<EncodeTiled>(p);
+    return ONEBIT_OK;
+}
+
+// The codes as rows of bytes, taken in boxes of 128 bytes by `box` rows; zeros behind the edges.
+int codes_map(EncodeTiled encode, CUtensorMap* map, const void* codes, int64_t rows, int64_t cols,
+              int box) {
+    const cuuint64_t dims[2] = {(cuuint64_t)mx4_pitch(cols), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)mx4_pitch(cols)};
+    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims,
+                              strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ONEBIT_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+struct MmOperands {
+    const void *a, *b;
+    int64_t m, n, k;
+    Mx4MatmulArgs args;
+};
+
+template <int TM, typename OT, bool SPLIT>
+int launch_mx4_matmul(const MmOperands& o, int split, cudaStream_t st) {
+    using S = MmTile<TM>;
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = k_mx4_matmul<TM, OT, SPLIT>;
+    ONEBIT_CUDA(allow_smem(kernel, S::kSmem, done));
+    EncodeTiled encode;
+    int rc = encode_tiled(&encode);
+    if (rc != ONEBIT_OK) return rc;
+    CUtensorMap ma, mb;
+    rc = codes_map(encode, &ma, o.a, o.m, o.k, TM);
+    if (rc == ONEBIT_OK) rc = codes_map(encode, &mb, o.b, o.n, o.k, kMmLanes);
+    if (rc != ONEBIT_OK) return rc;
+    const int64_t tiles = (int64_t)o.args.tiles_m * o.args.tiles_n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : std::min<int64_t>(tiles, kSms)));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    if (SPLIT) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    ONEBIT_CUDA(cudaLaunchKernelEx(&cfg, kernel, ma, mb, o.args));
+    return ONEBIT_OK;
+}
+
+template <int TM, typename OT>
+int queue_mx4_matmul(MmOperands o, cudaStream_t st) {
+    o.args.tiles_m = (int32_t)ceil_div(o.m, TM);
+    o.args.tiles_n = (int32_t)ceil_div(o.n, kMmLanes);
+    const int64_t tiles = (int64_t)o.args.tiles_m * o.args.tiles_n;
+    const int split =
+        (int)std::min<int64_t>(std::min<int64_t>(8, kSms / tiles), (int64_t)o.args.stages);
+    if (split > 1) return launch_mx4_matmul<TM, OT, true>(o, split, st);
+    return launch_mx4_matmul<TM, OT, false>(o, 1, st);
+}
+
+template <typename OT>
+int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
+    if (o.m <= 16) return queue_mx4_matmul<16, OT>(o, st);
+    if (o.m <= 32) return queue_mx4_matmul<32, OT>(o, st);
+    if (o.m <= 64) return queue_mx4_matmul<64, OT>(o, st);
+    if (o.m <= 128) return queue_mx4_matmul<128, OT>(o, st);
+    return queue_mx4_matmul<256, OT>(o, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int onebit_mx4_layout(int64_t rows, int64_t cols, int64_t* code_bytes, int64_t* scale_bytes) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_mx4_layout";
+        const int rc = mx4_shape(where, rows, cols);
+        if (rc != ONEBIT_OK) return rc;
+        if (code_bytes == nullptr || scale_bytes == nullptr) return bad(where, "null result");
+        *code_bytes = mx4_code_bytes(rows, cols);
+        *scale_bytes = mx4_scale_bytes(rows, cols);
+        return ONEBIT_OK;
+    });
+}
+
+int onebit_mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype, int64_t ld,
+                        uint8_t* codes, uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t,
+                        int32_t stochastic, uint64_t seed, float* residual, int64_t ld_residual,
+                        void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_mx4_quantize";
+        int rc = mx4_shape(where, rows, cols);
+        if (rc != ONEBIT_OK) return rc;
+        if (!known_dtype(dtype)) return bad(where, "unknown type");
+        if (stochastic != 0 && stochastic != 1) return bad(where, "stochastic must be 0 or 1");
+        if (rows == 0 || cols == 0) return ONEBIT_OK;
+        if (codes == nullptr && codes_t == nullptr) return bad(where, "neither codes nor codes_t");
+        if (residual != nullptr && (codes == nullptr || codes_t != nullptr))
+            return bad(where, "a residual goes with codes alone");
+        rc = mx4_plain(where, "x", rows, cols, x, ld, width(dtype));
+        if (rc == ONEBIT_OK && codes != nullptr) rc = mx4_matrix(where, rows, cols, codes, scales);
+        if (rc == ONEBIT_OK && codes_t != nullptr)
+            rc = mx4_matrix(where, cols, rows, codes_t, scales_t);
+        if (rc == ONEBIT_OK && residual != nullptr)
+            rc = mx4_plain(where, "residual", rows, cols, residual, ld_residual, 4);
+        if (rc != ONEBIT_OK) return rc;
+        if (mx4_atoms(rows) * mx4_atoms(cols) > ((int64_t)1 << 29)) return bad(where, "bad size of a matrix");
+        Ranges ranges;
+        ranges.add(0, x, mx4_span(rows, cols, ld, width(dtype)), false);
+        if (codes != nullptr) {
+            ranges.add(1, codes, mx4_code_bytes(rows, cols), true);
+            ranges.add(1, scales, mx4_scale_bytes(rows, cols), true);
+        }
+        if (codes_t != nullptr) {
+            ranges.add(2, codes_t, mx4_code_bytes(cols, rows), true);
+            ranges.add(2, scales_t, mx4_scale_bytes(cols, rows), true);
+        }
+        if (residual != nullptr) ranges.add(3, residual, mx4_span(rows, cols, ld_residual, 4), true);
+        if (ranges.clash()) return bad(where, "what is written overlaps something else");
+        Mx4QuantArgs a{};
+        a.x = x;
+        a.ld = ld;
+        a.rows = rows;
+        a.cols = cols;
+        a.e = residual;
+        a.lde = ld_residual;
+        a.c = codes;
+        a.s = scales;
+        a.ct = codes_t;
+        a.st = scales_t;
+        a.seed = seed;
+        a.col_tiles = mx4_atoms(cols);
+        a.vec = aligned_to(x, 8 * width(dtype)) && (rows == 1 || ld % 8 == 0);
+        a.vece = aligned_to(residual, 32) && (rows == 1 || ld_residual % 8 == 0);
+        const cudaStream_t st = as_stream(stream);
+        if (dtype == ONEBIT_F32)
+            return stochastic ? queue_mx4_quantize<float, true>(a, st)
+                              : queue_mx4_quantize<float, false>(a, st);
+        return stochastic ? queue_mx4_quantize<__nv_bfloat16, true>(a, st)
+                          : queue_mx4_quantize<__nv_bfloat16, false>(a, st);
+    });
+}
+
+int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
+                          void* out, int32_t dtype, int64_t ld, void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_mx4_dequantize";
+        int rc = mx4_shape(where, rows, cols);
+        if (rc != ONEBIT_OK) return rc;
+        if (!known_dtype(dtype)) return bad(where, "unknown type");
+        rc = mx4_matrix(where, rows, cols, codes, scales);
+        if (rc == ONEBIT_OK) rc = mx4_plain(where, "out", rows, cols, out, ld, width(dtype));
+        if (rc != ONEBIT_OK || rows == 0 || cols == 0) return rc;
+        if (mx4_atoms(rows) * mx4_atoms(cols) > ((int64_t)1 << 29)) return bad(where, "bad size of a matrix");
+        Ranges ranges;
+        ranges.add(0, codes, mx4_code_bytes(rows, cols), false);
+        ranges.add(1, scales, mx4_scale_bytes(rows, cols), false);
+        ranges.add(2, out, mx4_span(rows, cols, ld, width(dtype)), true);
+        if (ranges.clash()) return bad(where, "out overlaps the codes or exponents");
+        const Mx4DequantArgs a{codes, scales, out, ld, rows, cols, mx4_atoms(cols),
+                               aligned_to(out, 8 * width(dtype)) && (rows == 1 || ld % 8 == 0)};
+        constexpr int kRows = 32;
+        const unsigned blocks = (unsigned)(a.col_tiles * ceil_div(rows, kRows));
+        if (dtype == ONEBIT_F32)
+            k_mx4_dequantize<float, kRows><<<blocks, kMxThreads, 0, as_stream(stream)>>>(a);
+        else
+            k_mx4_dequantize<__nv_bfloat16, kRows><<<blocks, kMxThreads, 0, as_stream(stream)>>>(a);
+        ONEBIT_CUDA(cudaGetLastError());
+        return ONEBIT_OK;
+    });
+}
+
+int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
+                      const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
+                      void* out, int32_t dtype, int64_t ld, int32_t accumulate, void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_mx4_matmul";
+        int rc = mx4_shape(where, m, k);
+        if (rc == ONEBIT_OK) rc = mx4_shape(where, n, k);
+        if (rc != ONEBIT_OK) return rc;
+        if (!known_dtype(dtype)) return bad(where, "unknown type");
+        if (accumulate != 0 && accumulate != 1) return bad(where, "accumulate must be 0 or 1");
+        if (accumulate && dtype != ONEBIT_F32) return bad(where, "accumulation needs a float32 out");
+        if (m == 0 || n == 0) return ONEBIT_OK;
+        rc = mx4_matrix(where, m, k, a_codes, a_scales);
+        if (rc == ONEBIT_OK) rc = mx4_matrix(where, n, k, b_codes, b_scales);
+        if (rc == ONEBIT_OK) rc = mx4_plain(where, "out", m, n, out, ld, width(dtype));
+        if (rc != ONEBIT_OK) return rc;
+        Ranges ranges;
+        if (k > 0) {
+            ranges.add(0, a_codes, mx4_code_bytes(m, k), false);
+            ranges.add(0, a_scales, mx4_scale_bytes(m, k), false);
+            ranges.add(1, b_codes, mx4_code_bytes(n, k), false);
+            ranges.add(1, b_scales, mx4_scale_bytes(n, k), false);
+        }
+        ranges.add(2, out, mx4_span(m, n, ld, width(dtype)), true);
+        if (ranges.clash()) return bad(where, "out overlaps an operand");
+        const cudaStream_t st = as_stream(stream);
+        if (k == 0) {
+            if (!accumulate)
+                ONEBIT_CUDA(cudaMemset2DAsync(out, (size_t)((m > 1 ? ld : n) * width(dtype)), 0,
+                                              (size_t)(n * width(dtype)), (size_t)m, st));
+            return ONEBIT_OK;
+        }
+        MmOperands o{a_codes, b_codes, m, n, k, {}};
+        o.args.sa = a_scales;
+        o.args.sb = b_scales;
+        o.args.out = out;
+        o.args.ld = ld;
+        o.args.m = (int32_t)m;
+        o.args.n = (int32_t)n;
+        o.args.steps = (int32_t)ceil_div(k, 64);
+        o.args.stages = (int32_t)ceil_div(k, kStageCols);
+        o.args.atoms = (int32_t)mx4_atoms(k);
+        o.args.accumulate = accumulate;
+        return dtype == ONEBIT_F32 ? queue_mx4_matmul<float>(o, st)
+                                   : queue_mx4_matmul<__nv_bfloat16>(o, st);
+    });
+}
+
+int onebit_mx4_status(uint32_t* flags, void* stream) {
+    return guarded([&]() -> int {
+        if (flags == nullptr) return bad("onebit_mx4_status", "null flags");
+        const cudaStream_t st = as_stream(stream);
+        ONEBIT_CUDA(cudaMemcpyFromSymbolAsync(flags, g_mx4_status, 4, 0, cudaMemcpyDeviceToHost, st));
+        ONEBIT_CUDA(cudaStreamSynchronize(st));
+        return ONEBIT_OK;
+    });
+}
+
+}  // extern "C"

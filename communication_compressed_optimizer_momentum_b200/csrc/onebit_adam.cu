@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>  // header-only; ranges are free unless a profiler is attached
 
+#include "host.h"
 #include "onebit_adam.h"
 #include "kernels.cuh"
 #include "kernels_dp.cuh"
@@ -31,30 +32,12 @@ using namespace onebit;
 
 namespace {
 
-thread_local std::string g_last_error;
-
 constexpr int32_t kMaxWorkers = 256;
 constexpr int kLaunchesPerStep = 5;
 constexpr int kLaunchesPerStepDp = 7;  // plus one barrier after each half of the exchange
 constexpr int kEventsPerStep = kLaunchesPerStep + 1;
 
 enum Phase { kUnbound = 0, kWarmup = 1, kCompressed = 2 };
-
-int cuda_fail(cudaError_t e) {
-    g_last_error = cudaGetErrorString(e);
-    return ONEBIT_ERR_CUDA;
-}
-
-#define ONEBIT_CUDA(call)                                 \
-    do {                                                  \
-        cudaError_t e_ = (call);                          \
-        if (e_ != cudaSuccess) return cuda_fail(e_);      \
-    } while (0)
-
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Workspace regions, each 256-byte aligned. For a data-parallel rank, m, v, bits_w, bits_s and
 // S_out have no space here (m, v, the server plane and scales live in the exchange region, the
@@ -1796,3 +1779,8 @@ extern "C" int onebit_compress_static(const float* x, int64_t n, int64_t C, uint
 // AdamW over a list of tensors
 
 #include "adamw.cuh"
+
+// ------------------------------------------------------------------------------------------
+// Matrices in microscaled 4-bit floating point
+
+#include "mx4.cuh"

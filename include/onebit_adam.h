@@ -27,6 +27,8 @@
  *   - onebit_pack, onebit_unpack, onebit_compress_static: one vector's 1-bit message;
  *   - onebit_adamw_*, onebit_adamw8_*, onebit_grad_norm: AdamW over a list of tensors, with
  *     states in 32 or in 8 bits, and the global gradient norm that clips its gradients;
+ *   - onebit_mx4_*: matrices in microscaled 4-bit floating point: quantising (also with error
+ *     feedback), reading back and products;
  *   - host-only queries: onebit_dp_chunk_range, onebit_server_layout, onebit_strerror,
  *     onebit_last_error.
  *
@@ -673,6 +675,77 @@ int onebit_adamw8_set_state(int64_t total, uint8_t* m, uint8_t* v, uint8_t* m_ex
 int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* grads,
                      int32_t grad_dtype, double max_norm, int32_t accumulate, void* work,
                      void* stream);
+
+/*
+ * ------------------------------------------------------------------------------------------
+ * Matrices in microscaled 4-bit floating point: what a linear layer's weights, activations and
+ * gradients become for products on the 4-bit tensor cores, and a message of 4.25 bits a value with
+ * error feedback. No handle; the caller owns every buffer and nothing is kept between calls.
+ *
+ * A matrix of rows x cols (each at most 2^30) is held as
+ *   codes:  uint8 [rows][16 * ceil(cols / 32)], two codes a byte, the even column in the lower four
+ *           bits. A code is a sign (8), two exponent bits and one mantissa bit: codes 0 to 7 stand for
+ *           0, 0.5, 1, 1.5, 2, 3, 4, 6. Columns behind the last hold 0.
+ *   scales: a byte s for each block of 32 consecutive columns of a row, which multiplies the codes by
+ *           2^(s-127); 255 makes the whole block NaN. Tiles of 128 rows by 4 blocks, 512 bytes each,
+ *           all tiles of 128 rows one after another: row r, block b at
+ *           ((r/128) * ceil(cols/128) + b/4) * 512 + (r%32) * 16 + (r%128/32) * 4 + b%4.
+ *           Places of no block hold 0.
+ * both 16-byte aligned, of the lengths that onebit_mx4_layout gives.
+ *
+ * Quantising a block: a = its largest magnitude; 2^k the smallest power of two, k >= -127, with
+ * a <= 6 * 2^k (nothing saturates); an infinity, a NaN or a > 1.5 * 2^127 makes the block NaN.
+ * z = x / 2^k becomes the nearest of the codes' values, the even code if two are as near, or with
+ * stochastic = 1 one of its two neighbours: with the remainder r (0 <= r < 1) of |z| above the lower
+ * one, in units of their distance, the upper one if floor(65536 r) + u >= 65536. The mean is z, but
+ * for what 16 bits lose: low by 2^-17 of the distance on average. u, 16 bits, is a function of seed
+ * and of the element's place i = row * 32 * ceil(cols/32) + column in the matrix that is written
+ * (mix and G as for onebit_adamw8_step):
+ *   key = mix(mix(lo(seed) + G) ^ hi(seed)) ;  w = mix(lo(i/8) + key + hi(i/8) * G)
+ *   x = w + ((i%8)/2 + 1) * G ;  x ^= x>>15, x *= 0x8A8866C7, x ^= x>>16
+ *   u = i even: x>>16, odd: x & 0xffff
+ * Rows of a plain matrix are ld elements apart (ignored for one row); elements are aligned to
+ * themselves (eight of them, and ld a multiple of eight, are faster).
+ *
+ * Refused (ONEBIT_ERR_ARG, ONEBIT_ERR_ALIGN; the reason in onebit_last_error): what the above
+ * excludes, and buffers that are written and overlap another of the call. Empty matrices are
+ * valid; their pointers are ignored.
+ * ------------------------------------------------------------------------------------------
+ */
+
+/* Bytes of the codes and of the scales. Host only. */
+int onebit_mx4_layout(int64_t rows, int64_t cols, int64_t* code_bytes, int64_t* scale_bytes);
+
+/*
+ * Quantise x (fp32 or bf16 by dtype): codes and scales receive the matrix, codes_t and scales_t its
+ * transpose (cols x rows, blocks along x's rows; its random bits are those of seed + 1). Either
+ * codes or codes_t may be NULL; both are written from one pass over x.
+ * residual (or NULL; fp32 [rows][ld_residual], with codes alone): error feedback. y = x + residual
+ * (one fp32 addition) is quantised instead of x, and residual = y - its value (one fp32 subtraction,
+ * exact when rounding to nearest; NaN in a NaN block).
+ */
+int onebit_mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype, int64_t ld,
+                        uint8_t* codes, uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t,
+                        int32_t stochastic, uint64_t seed, float* residual, int64_t ld_residual,
+                        void* stream);
+
+/* What a matrix stands for, in fp32 or bf16 by dtype (exact in both). */
+int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
+                          void* out, int32_t dtype, int64_t ld, void* stream);
+
+/*
+ * out = a b^T, or out + a b^T with accumulate = 1 (fp32 only): a is m x k, b is n x k, both in 4
+ * bits; out [m][ld] fp32 or bf16 by dtype. Sums in fp32 on the tensor cores, in an order that the
+ * sizes alone fix; products below fp32's range are lost. A NaN block makes its row of a (its column
+ * of out, for b) NaN. k = 0 gives zeros (accumulate: out as it was).
+ */
+int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
+                      const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
+                      void* out, int32_t dtype, int64_t ld, int32_t accumulate, void* stream);
+
+/* *flags (host): 1 if a wait within a product on this device ever gave up (its result is then not
+ * valid), else 0. Waits for the stream. */
+int onebit_mx4_status(uint32_t* flags, void* stream);
 
 /* Static description of a status code. */
 const char* onebit_strerror(int32_t code);
