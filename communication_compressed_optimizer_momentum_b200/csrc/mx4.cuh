@@ -102,74 +102,109 @@ int encode_tiled(EncodeTiled* f) {
     return ONEBIT_OK;
 }
 
-// The codes as rows of bytes, taken in boxes of 128 bytes by `box` rows; zeros behind the edges.
-int codes_map(EncodeTiled encode, CUtensorMap* map, const void* codes, int64_t rows, int64_t cols,
-              int box) {
-    const cuuint64_t dims[2] = {(cuuint64_t)mx4_pitch(cols), (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)mx4_pitch(cols)};
-    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims,
-                              strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+// A matrix of rows of `width` elements, `ld` apart, taken in boxes; zeros behind the edges.
+int box_map(EncodeTiled encode, CUtensorMap* map, CUtensorMapDataType type, int64_t bytes,
+            const void* base, int64_t width, int64_t rows, int64_t ld, int across, int down,
+            CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * bytes)};
+    const cuuint32_t box[2] = {(cuuint32_t)across, (cuuint32_t)down}, ones[2] = {1, 1};
+    const CUresult r = encode(map, type, 2, const_cast<void*>(base), dims, strides, box, ones,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ONEBIT_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
+// The codes as rows of bytes, in boxes of 128 bytes by `box` rows, and the exponents as a row of words
+// for each 128 rows, in boxes of two atoms by `atoms` rows. (Exponents as plain bulk copies of 1 KB, of
+// which a stage takes three, hold up the loads.)
+int operand_maps(EncodeTiled encode, CUtensorMap* codes_map, CUtensorMap* scales_map,
+                 const void* codes, const void* scales, int64_t rows, int64_t cols, int box,
+                 int atoms) {
+    const int rc = box_map(encode, codes_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, mx4_pitch(cols),
+                           rows, mx4_pitch(cols), 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != ONEBIT_OK) return rc;
+    return box_map(encode, scales_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, scales,
+                   mx4_atoms(cols) * (kAtomBytes / 4), mx4_atoms(rows),
+                   mx4_atoms(cols) * (kAtomBytes / 4), 2 * kAtomBytes / 4, atoms,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 struct MmOperands {
-    const void *a, *b;
+    const void *a, *sa, *b, *sb;
     int64_t m, n, k;
     Mx4MatmulArgs args;
 };
 
-template <int TM, typename OT, bool SPLIT>
-int launch_mx4_matmul(const MmOperands& o, int split, cudaStream_t st) {
-    using S = MmTile<TM>;
+template <int TM, bool PAIR, typename OT, bool SPLIT>
+int launch_mx4_matmul(MmOperands o, int split, cudaStream_t st) {
+    using S = MmTile<TM, PAIR, SPLIT>;
     static std::atomic<uint64_t> done{0};
-    const auto kernel = k_mx4_matmul<TM, OT, SPLIT>;
+    const auto kernel = k_mx4_matmul<TM, PAIR, OT, SPLIT>;
     ONEBIT_CUDA(allow_smem(kernel, S::kSmem, done));
     EncodeTiled encode;
     int rc = encode_tiled(&encode);
     if (rc != ONEBIT_OK) return rc;
-    CUtensorMap ma, mb;
-    rc = codes_map(encode, &ma, o.a, o.m, o.k, TM);
-    if (rc == ONEBIT_OK) rc = codes_map(encode, &mb, o.b, o.n, o.k, kMmLanes);
+    Mx4Maps maps;
+    rc = operand_maps(encode, &maps.a, &maps.sa, o.a, o.sa, o.m, o.k, S::kARows, S::kHalves);
+    if (rc == ONEBIT_OK)
+        rc = operand_maps(encode, &maps.b, &maps.sb, o.b, o.sb, o.n, o.k, kMmLanes, 1);
+    if (rc == ONEBIT_OK && o.args.tma) {
+        constexpr bool wide = sizeof(OT) == 4;
+        rc = box_map(encode, &maps.out, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     sizeof(OT), o.args.out, o.n, o.m, o.m > 1 ? o.args.ld : round_up(o.n, 8), 32,
+                     wide ? kOutRows32 : 32,
+                     wide ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B);
+    }
     if (rc != ONEBIT_OK) return rc;
+    o.args.tiles_m = (int32_t)ceil_div(o.m, TM);
+    o.args.tiles_n = (int32_t)ceil_div(o.n, kMmLanes * S::kGroup);
     const int64_t tiles = (int64_t)o.args.tiles_m * o.args.tiles_n;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : std::min<int64_t>(tiles, kSms)));
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split
+                                        : std::min<int64_t>(tiles, kSms / S::kGroup) * S::kGroup));
     cfg.blockDim = dim3(kMmThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
-    if (SPLIT) {
+    if (PAIR || SPLIT) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.x = (unsigned)(PAIR ? 2 : split);
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    ONEBIT_CUDA(cudaLaunchKernelEx(&cfg, kernel, ma, mb, o.args));
+    ONEBIT_CUDA(cudaLaunchKernelEx(&cfg, kernel, maps, o.args));
     return ONEBIT_OK;
-}
-
-template <int TM, typename OT>
-int queue_mx4_matmul(MmOperands o, cudaStream_t st) {
-    o.args.tiles_m = (int32_t)ceil_div(o.m, TM);
-    o.args.tiles_n = (int32_t)ceil_div(o.n, kMmLanes);
-    const int64_t tiles = (int64_t)o.args.tiles_m * o.args.tiles_n;
-    const int split =
-        (int)std::min<int64_t>(std::min<int64_t>(8, kSms / tiles), (int64_t)o.args.stages);
-    if (split > 1) return launch_mx4_matmul<TM, OT, true>(o, split, st);
-    return launch_mx4_matmul<TM, OT, false>(o, 1, st);
 }
 
 template <typename OT>
 int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
-    if (o.m <= 16) return queue_mx4_matmul<16, OT>(o, st);
-    if (o.m <= 32) return queue_mx4_matmul<32, OT>(o, st);
-    if (o.m <= 64) return queue_mx4_matmul<64, OT>(o, st);
-    if (o.m <= 128) return queue_mx4_matmul<128, OT>(o, st);
-    return queue_mx4_matmul<256, OT>(o, st);
+    const int64_t tn = ceil_div(o.n, kMmLanes), stages = o.args.stages;
+    // Few rows: narrow tiles; what they leave idle takes parts of the common axis.
+    const auto spare = [&](int tm) {
+        return (int)std::min<int64_t>(std::min<int64_t>(8, kSms / (tn * ceil_div(o.m, tm))), stages);
+    };
+    if (o.m <= 16) {
+        const int split = spare(16);
+        if (split > 1) return launch_mx4_matmul<16, false, OT, true>(o, split, st);
+        return launch_mx4_matmul<16, false, OT, false>(o, 1, st);
+    }
+    // Rounds of tiles times a tile's clocks: a stage's, measured, and its share of the writing out.
+    const auto cost = [&](int tm, int group, int64_t stage, int64_t tile) {
+        const int64_t tiles = ceil_div(o.m, tm) * ceil_div(o.n, kMmLanes * group);
+        return ceil_div(tiles, kSms / group) * (stages * stage + tile);
+    };
+    const int64_t c32 = cost(32, 1, 400, 600), c64 = cost(64, 1, 460, 900),
+                  c128 = cost(128, 1, 600, 1500), c256 = cost(256, 2, 640, 2500);
+    const int64_t best = std::min(std::min(c32, c64), std::min(c128, c256));
+    if (best == c256) return launch_mx4_matmul<256, true, OT, false>(o, 1, st);
+    if (best == c128) return launch_mx4_matmul<128, false, OT, false>(o, 1, st);
+    if (best == c64) return launch_mx4_matmul<64, false, OT, false>(o, 1, st);
+    const int split = spare(32);
+    if (split > 1) return launch_mx4_matmul<32, false, OT, true>(o, split, st);
+    return launch_mx4_matmul<32, false, OT, false>(o, 1, st);
 }
 
 }  // namespace
@@ -307,17 +342,16 @@ int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
                                               (size_t)(n * width(dtype)), (size_t)m, st));
             return ONEBIT_OK;
         }
-        MmOperands o{a_codes, b_codes, m, n, k, {}};
-        o.args.sa = a_scales;
-        o.args.sb = b_scales;
+        MmOperands o{a_codes, a_scales, b_codes, b_scales, m, n, k, {}};
         o.args.out = out;
         o.args.ld = ld;
         o.args.m = (int32_t)m;
         o.args.n = (int32_t)n;
         o.args.steps = (int32_t)ceil_div(k, 64);
         o.args.stages = (int32_t)ceil_div(k, kStageCols);
-        o.args.atoms = (int32_t)mx4_atoms(k);
         o.args.accumulate = accumulate;
+        o.args.tma = aligned16(out) && (m == 1 || ld * width(dtype) % 16 == 0);
+        if (ceil_div(m, 16) * ceil_div(n, kMmLanes) > (1 << 30)) return bad(where, "out is too large");
         return dtype == ONEBIT_F32 ? queue_mx4_matmul<float>(o, st)
                                    : queue_mx4_matmul<__nv_bfloat16>(o, st);
     });
