@@ -11,6 +11,8 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,56 +72,171 @@ __device__ __forceinline__ uint32_t encode8_nearest(const float (&z)[8]) {
     return r;
 }
 
-// Eight codes, rounded up with the probability of the remainder in 16 bits. |z| * 2^-126 (rounded
-// toward zero: a remainder keeps 22 bits) lines the codes up with the upper bits of an fp32 pattern,
+// Eight codes, rounded up with the probability of the remainder in 16 bits. y = z * 2^-126 (rounded
+// toward zero: a remainder keeps 22 bits) lines the codes up with bits 24 to 22 of an fp32 pattern,
 // subnormal ones too; the random bits are added below them. |z| <= 6 cannot carry beyond the largest
-// code. w: the random word of the group of eight.
-__device__ __forceinline__ uint32_t encode8_stochastic(const float (&z)[8], uint32_t w) {
+// code. w: the random word of the group of eight. Instructions bound it, 14 a value: the integer ones
+// that make the random bits most of all.
+__device__ __forceinline__ uint32_t encode8_stochastic(const float (&y)[8], uint32_t w) {
     uint32_t r = 0;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 3; p >= 0; --p) {
         uint32_t x = w + (uint32_t)(p + 1) * kGolden;
         x ^= x >> 15;
         x *= 0x8A8866C7u;
-        x ^= x >> 16;
+        const uint32_t u[2] = {x >> 16, (x ^ (x >> 16)) & 0xffffu};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = 2 * p + h;
-            const uint32_t y = __float_as_uint(__fmul_rz(fabsf(z[i]), 0x1p-126f));
-            const uint32_t add = h == 0 ? (x >> 16) << 6 : (x & 0xffffu) << 6;
-            r |= ((y + add) >> 22) << (4 * i);
-            r |= (__float_as_uint(z[i]) >> 31) << (4 * i + 3);
+        for (int h = 1; h >= 0; --h) {
+            const uint32_t t = __float_as_uint(y[2 * p + h]) + u[h] * 64u;
+            r = __funnelshift_l((t << 6) | (t & 0x80000000u), r, 4);   // sign and code on top
         }
     }
     return r;
 }
 
-// The key of the random bits, and the word of the group of eight places that begins at place 8 G.
-__device__ __forceinline__ uint32_t mx4_key(uint64_t seed) {
-    return mix32(mix32((uint32_t)seed + kGolden) ^ (uint32_t)(seed >> 32));
-}
-
+// Eight values to codes in a block of exponent k; w: the random word.
 template <bool SR>
-__device__ __forceinline__ uint32_t encode8(const float (&z)[8], uint32_t key, int64_t G) {
-    if constexpr (SR)
-        return encode8_stochastic(z, group_word(key, G));
-    else
-        return encode8_nearest(z);
+__device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t k, uint32_t w) {
+    float z[8];
+    uint32_t c;
+    if constexpr (SR) {
+        // one factor where fp32 has it, 2^(1 - k)
+        if (k <= 127u) {
+            const float f = k == 0u ? 2.0f : __uint_as_float((128u - k) << 23);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = __fmul_rz(v[i], f);
+        } else {
+            const float inv = mx4_inverse(k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = __fmul_rz(v[i] * inv, 0x1p-126f);
+        }
+        c = encode8_stochastic(z, w);
+    } else {
+        const float inv = mx4_inverse(k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = v[i] * inv;
+        c = encode8_nearest(z);
+    }
+    return k == kMxNan ? 0u : c;
 }
 
-// What eight codes stand for, but for the block's power of two.
-__device__ __forceinline__ void decode8(uint32_t c, float (&o)[8]) {
+// Largest magnitudes by their patterns: any NaN is above infinity.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A block of 32 values, as it is loaded.
+template <typename T>
+struct Values;
+template <>
+struct Values<float> {
+    float v[32];
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    __device__ __forceinline__ uint32_t most() const {
+        float m[4] = {fabsf(v[0]), fabsf(v[1]), fabsf(v[2]), fabsf(v[3])};
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        uint32_t h;
-        asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n"
-            " cvt.rn.f16x2.e2m1x2 %0, a;\n}\n"
-            : "=r"(h)
-            : "r"(c >> (8 * p)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        o[2 * p] = f.x;
-        o[2 * p + 1] = f.y;
+        for (int i = 4; i < 32; ++i) m[i & 3] = max_nan(m[i & 3], fabsf(v[i]));
+        return __float_as_uint(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]))) & 0x7fffffffu;
     }
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float t[8];
+            ld8(p + 8 * g, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * g + i] = t[i];
+        }
+    }
+    __device__ __forceinline__ void load_some(const float* p, int n) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < n ? p[i] : 0.0f;
+    }
+};
+template <>
+struct Values<__nv_bfloat16> {
+    uint32_t w[16];
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ uint32_t most() const {
+        uint32_t m[2] = {w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu};
+#pragma unroll
+        for (int i = 2; i < 16; ++i) m[i & 1] = max_u16x2(m[i & 1], w[i] & 0x7fff7fffu);
+        const uint32_t x = max_u16x2(m[0], m[1]);
+        return max(x << 16, x & 0xffff0000u);
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(w[8 * g]), "=r"(w[8 * g + 1]), "=r"(w[8 * g + 2]),
+                           "=r"(w[8 * g + 3]), "=r"(w[8 * g + 4]), "=r"(w[8 * g + 5]),
+                           "=r"(w[8 * g + 6]), "=r"(w[8 * g + 7])
+                         : "l"(p + 16 * g));
+    }
+    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int n) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i] = (2 * i < n ? q[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+    }
+};
+
+// Codes of a block of exponent k; get(i): its values; G: its first place / 8; key: of the random bits.
+template <bool SR, typename F>
+__device__ __forceinline__ uint4 encode32(F&& get, uint32_t k, uint32_t key, int64_t G) {
+    const uint32_t kh = SR ? key + (uint32_t)(G >> 32) * kGolden : 0u;
+    uint32_t w[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = get(8 * g + i);
+        w[g] = encode8<SR>(v, k, SR ? mix32((uint32_t)G + g + kh) : 0u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The same with the exponent that the block takes.
+template <bool SR, typename V>
+__device__ __forceinline__ uint4 encode_block(const V& v, uint32_t key, int64_t G, uint32_t& k) {
+    k = mx4_exponent(v.most());
+    return encode32<SR>([&](int i) { return v.get(i); }, k, key, G);
+}
+
+// Eight codes (a word) as bf16 values times a power of two: both bytes of a magnitude come from a
+// table of eight, the signs go on top. Exact: bf16 holds every such value.
+__device__ __forceinline__ uint4 decode8(uint32_t c, uint32_t scale2) {
+    uint32_t o[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t x = h == 0 ? c : c >> 16, sel = x & 0x7777u;
+        const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, sel);
+        const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, sel);
+        const uint32_t even = __byte_perm(lo, hi, 0x5140) | ((x & 0x8u) << 12) | ((x & 0x80u) << 24);
+        const uint32_t odd =
+            __byte_perm(lo, hi, 0x7362) | ((x & 0x800u) << 4) | ((x & 0x8000u) << 16);
+        const uint32_t two[2] = {even, odd};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * h + i]) : "r"(two[i]), "r"(scale2));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// 2^(k - 127), NaN for a NaN block, twice in bf16.
+__device__ __forceinline__ uint32_t mx4_scale2(uint32_t k) {
+    const uint32_t h = k == kMxNan ? 0x7fffu : k > 0u ? k << 7 : 0x0040u;
+    return h | h << 16;
+}
+__device__ __forceinline__ float bf16_at(const uint4& w, int i) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    return __uint_as_float((i & 1) ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
 }
 
 struct Mx4QuantArgs {
@@ -129,193 +246,381 @@ struct Mx4QuantArgs {
     int64_t lde;
     uint8_t *c, *s;            // the matrix: codes and exponents
     uint8_t *ct, *st;          // the transposed matrix
-    uint64_t seed;             // of the matrix; the transposed one's is one more
-    int64_t col_tiles;
-    int32_t vec, vece;         // whole groups of eight are aligned for ld8
+    uint32_t key, tkey;        // of the random bits: the matrix's, the transposed one's
+    int64_t col_tiles;         // of 128
+    // k_mx4_rows: thread blocks take `rows_per` rows (segments = 1), or `segment` blocks of one row
+    int32_t segments, segment, rows_per;
+    uint32_t magic;            // 2^32 / (blocks of a row, up to a multiple of four), rounded up
 };
-
-// Eight consecutive values from column `col` on, zeros behind the last.
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int64_t col, int64_t cols, bool vec,
-                                      float (&o)[8]) {
-    if (vec && col + 8 <= cols) {
-        ld8(row + col, o);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = col + i < cols ? ld1(row + col + i) : 0.0f;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void keep8(T* p, const float (&o)[8]);
-template <>
-__device__ __forceinline__ void keep8(float* p, const float (&o)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
-}
-template <>
-__device__ __forceinline__ void keep8(__nv_bfloat16* p, const float (&o)[8]) {
-    st8(p, o);
-}
 
 constexpr int kMxRows = 1, kMxColumns = 2;   // forms
 constexpr int kMxThreads = 256;
 
-template <typename T>
-__host__ __device__ constexpr int mx4_tile_bytes() {
-    return kAtomRows * kAtomCols * (int)sizeof(T);
-}
-template <typename T, int FORMS>
-__host__ __device__ constexpr int mx4_quant_smem() {
-    return (FORMS & kMxColumns) ? mx4_tile_bytes<T>() + kAtomRows * 64 + kAtomBytes : 0;
-}
-
-// A block of a column of the tile (32 rows from `rb` blocks on), eight at a time.
-template <bool SR>
-__device__ __forceinline__ uint4 encode_block(const float (&v)[32], uint32_t key, int64_t G,
-                                              uint32_t& k) {
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
-    k = mx4_exponent(most);
-    const float inv = mx4_inverse(k);
-    uint32_t w[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = v[8 * g + i] * inv;
-        w[g] = k == kMxNan ? 0u : encode8<SR>(z, key, G + g);
+// The matrix itself, from rows whose blocks are aligned to 32 bytes. A thread takes UNITS of what is 32
+// bytes or more: bf16 a whole block, so that nothing is exchanged (8192 x 8192: 27 us; eight values a
+// thread, whose instructions bound it: 48); fp32, or with a residual, eight values, four lanes a block,
+// so that a warp's accesses are contiguous (a block a thread, whose accesses touch each line of memory
+// four times: 51 us against 45).
+struct MxPlace {
+    int64_t row;
+    int b;
+    bool in;
+};
+// Block `slot` of this thread block.
+__device__ __forceinline__ MxPlace mx4_place(int slot, int wide, int32_t segments, int32_t segment,
+                                             int32_t rows_per, uint32_t magic, int64_t rows) {
+    MxPlace p;
+    if (segments == 1) {
+        const int r = magic != 0 ? (int)__umulhi((uint32_t)slot, magic) : slot;
+        p.b = slot - r * wide;
+        p.row = (int64_t)blockIdx.x * rows_per + r;
+        p.in = r < rows_per && p.row < rows;
+    } else {
+        const uint32_t row = blockIdx.x / (uint32_t)segments;
+        p.row = row;
+        p.b = (int)(blockIdx.x - row * (uint32_t)segments) * segment + slot;
+        p.in = slot < segment && p.b < wide;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return p;
 }
 
-// One thread block takes ROWS x 128 values: of 128 rows, an atom of exponents in either form. Rows:
-// 16 lanes a row, eight columns a lane, four lanes a block. Columns: the values pass through shared
-// memory and a thread takes blocks of 32 rows; the codes go out through shared memory as well, so
-// that 64 bytes of a row of the transposed matrix are written together.
-template <typename T, int FORMS, bool SR, bool RES, int ROWS>
-__global__ void __launch_bounds__(kMxThreads) k_mx4_quantize(const Mx4QuantArgs a) {
-    static_assert(!(FORMS & kMxColumns) || ROWS == kAtomRows, "blocks of 32 rows");
-    static_assert(!RES || FORMS == kMxRows, "the residual is the rows' form's");
-    extern __shared__ __align__(128) uint8_t sm[];
-    T* tile = reinterpret_cast<T*>(sm);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t ct = blockIdx.x % a.col_tiles, rt = blockIdx.x / a.col_tiles;
-    const int64_t r0 = rt * ROWS, c0 = ct * kAtomCols;
-    const T* x = static_cast<const T*>(a.x);
-    const int sub = lane >> 4, g = lane & 15;
-    const int64_t col = c0 + g * 8;
+template <bool SR>
+__global__ void __launch_bounds__(kMxThreads) k_mx4_rows(const Mx4QuantArgs a) {
+    const int wide = (int)a.col_tiles * 4;          // blocks of a row, those of no column among them
+    const MxPlace t = mx4_place(threadIdx.x, wide, a.segments, a.segment, a.rows_per, a.magic,
+                                mx4_atoms(a.rows) * kAtomRows);
+    if (!t.in) return;
+    const int64_t pitch = mx4_pitch(a.cols), col = (int64_t)t.b * kMxBlk;
+    uint32_t k = 0;
+    if (t.row < a.rows && col < a.cols) {
+        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + t.row * a.ld + col;
+        const int n = (int)min(a.cols - col, (int64_t)kMxBlk);
+        Values<__nv_bfloat16> v;
+        if (n == kMxBlk)
+            v.load(x);
+        else
+            v.load_some(x, n);
+        *reinterpret_cast<uint4*>(a.c + t.row * pitch + col / 2) =
+            encode_block<SR>(v, a.key, (t.row * pitch) / 4 + t.b * 4, k);
+    }
+    a.s[((t.row >> 7) * a.col_tiles + (t.b >> 2)) * kAtomBytes + atom_at((int)(t.row & 127), t.b & 3)] =
+        (uint8_t)k;
+}
+
+// Eight values from `col` on, zeros from `cols` on.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t left, float (&o)[8]) {
+    if (left >= 8) {
+        ld8(p, o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = i < left ? ld1(p + i) : 0.0f;
+    }
+}
+
+// Eight values of a block that four lanes share: codes and the block's exponent.
+template <bool SR>
+__device__ __forceinline__ uint32_t encode_quarter(const float (&v)[8], uint32_t key, int64_t G,
+                                                   uint32_t& k) {
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
+    uint32_t most = __float_as_uint(m) & 0x7fffffffu;
+    most = max(most, __shfl_xor_sync(kFull, most, 1));
+    most = max(most, __shfl_xor_sync(kFull, most, 2));
+    k = mx4_exponent(most);
+    return encode8<SR>(v, k, SR ? group_word(key, G) : 0u);
+}
+
+constexpr int kMxUnits = 2;
+
+template <typename T, bool SR, bool RES>
+__global__ void __launch_bounds__(kMxThreads) k_mx4_rows8(const Mx4QuantArgs a) {
+    const int wide = (int)a.col_tiles * 4, g = threadIdx.x & 3;
     const int64_t pitch = mx4_pitch(a.cols);
-    const uint32_t key = SR ? mx4_key(a.seed) : 0u;
-    constexpr int kIter = ROWS / 16, kBatch = kIter < 4 ? kIter : 4;
-#pragma unroll 1
-    for (int it = 0; it < kIter; it += kBatch) {
-        float v[kBatch][8], e[RES ? kBatch : 1][8];
+    MxPlace t[kMxUnits];
+    float v[kMxUnits][8], e[RES ? kMxUnits : 1][8];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = (it + u) * 16 + warp * 2 + sub;
-            const int64_t row = r0 + r;
-            const bool in = row < a.rows;
-            load8(x + (in ? row * a.ld : 0), col, in ? a.cols : 0, a.vec, v[u]);
-            if constexpr (RES) load8(a.e + (in ? row * a.lde : 0), col, in ? a.cols : 0, a.vece, e[u]);
+    for (int u = 0; u < kMxUnits; ++u) {
+        t[u] = mx4_place((int)threadIdx.x / 4 + u * (kMxThreads / 4), wide, a.segments, a.segment,
+                         a.rows_per, a.magic, mx4_atoms(a.rows) * kAtomRows);
+        const int64_t col = (int64_t)t[u].b * kMxBlk + 8 * g;
+        const int64_t left = t[u].in && t[u].row < a.rows ? a.cols - col : 0;
+        load8(static_cast<const T*>(a.x) + t[u].row * a.ld + col, left, v[u]);
+        if constexpr (RES) load8(a.e + t[u].row * a.lde + col, left, e[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kMxUnits; ++u) {
+        const int64_t row = t[u].row;
+        const int b = t[u].b;
+        const int64_t col = (int64_t)b * kMxBlk + 8 * g;
+        const bool in = t[u].in && row < a.rows;
+        if constexpr (RES) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = __fadd_rn(v[u][i], e[u][i]);
         }
+        uint32_t k;
+        const uint32_t w = encode_quarter<SR>(v[u], a.key, (row * pitch) / 4 + b * 4 + g, k);
+        if (in && col / 2 < pitch) *reinterpret_cast<uint32_t*>(a.c + row * pitch + col / 2) = w;
+        if (t[u].in && g == 0)
+            a.s[((row >> 7) * a.col_tiles + (b >> 2)) * kAtomBytes + atom_at((int)(row & 127), b & 3)] =
+                (uint8_t)k;
+        if constexpr (RES) {
+            const uint4 q = decode8(w, mx4_scale2(k));
+            float o[8];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = (it + u) * 16 + warp * 2 + sub;
-            const int64_t row = r0 + r;
-            if constexpr (FORMS & kMxColumns) keep8(tile + r * kAtomCols + g * 8, v[u]);
-            if constexpr (FORMS & kMxRows) {
-                if constexpr (RES) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[u][i] = __fadd_rn(v[u][i], e[u][i]);
-                }
-                uint32_t most = 0;
+            for (int i = 0; i < 8; ++i) o[i] = __fsub_rn(v[u][i], bf16_at(q, i));
+            float* p = a.e + row * a.lde + col;
+            if (in && a.cols - col >= 8) {
+                st8(p, o);
+            } else if (in) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    most = max(most, __float_as_uint(v[u][i]) & 0x7fffffffu);
-                most = max(most, __shfl_xor_sync(kFull, most, 1));
-                most = max(most, __shfl_xor_sync(kFull, most, 2));
-                const uint32_t k = mx4_exponent(most);
-                const float inv = mx4_inverse(k);
-                float z[8];
+                    if (col + i < a.cols) p[i] = o[i];
+            }
+        }
+    }
+}
+
+// One thread block takes 128 rows by 128 (bf16) or 64 (fp32) columns, 32 KB. The values pass through
+// shared memory: for the transposed matrix a thread takes blocks of 32 rows, and its codes go out
+// through shared memory as well, so that 64 bytes of a row are written together. VEC: rows' blocks are
+// aligned to 32 bytes; they are loaded by 32 bytes and more a lane, and the matrix itself is made from
+// registers. Else the values are loaded one by one, consecutive lanes consecutive values.
+//
+// Shared memory holds a row as pieces of 16 bytes, which are swapped so that the eight lanes of a store
+// (bf16: two rows by four blocks; fp32: a row by eight quarters of blocks) put them into different
+// banks; 128 bytes of a row stay together, so that reading along it is free of conflicts too.
+template <typename V>
+struct MxTile {
+    static constexpr int kWide = sizeof(V) == 2 ? 128 : 64;   // columns
+    static constexpr int kBlocks = kWide / kMxBlk;
+    static constexpr int kParts = kAtomCols / kWide;          // tiles that share an atom of a row form
+    static constexpr int kBytes = kAtomRows * kWide * (int)sizeof(V);
+    static constexpr int kSmem = kBytes + kWide * 64 + 2 * kAtomBytes;
+    static __device__ __forceinline__ int piece(int row, int j) {
+        return sizeof(V) == 2 ? j ^ ((j >> 3) & 1) ^ ((row & 1) << 1) : j ^ ((j >> 3) & 1);
+    }
+    static __device__ __forceinline__ int at(int row, int col) {   // in values
+        constexpr int kPer = 16 / (int)sizeof(V);
+        return row * kWide + piece(row, col / kPer) * kPer + col % kPer;
+    }
+};
+
+__device__ __forceinline__ void mx4_kept(const float* tile, int r, int b, Values<float>& v) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = v[u][i] * inv;
-                const uint32_t w = k == kMxNan ? 0u : encode8<SR>(z, key, (row * pitch + col / 2) / 4);
-                if (row < a.rows && col / 2 < pitch)
-                    *reinterpret_cast<uint32_t*>(a.c + row * pitch + col / 2) = w;
-                if ((g & 3) == 0)
-                    a.s[((row >> 7) * a.col_tiles + ct) * kAtomBytes + atom_at((int)(row & 127), g >> 2)] =
-                        (uint8_t)k;
+    for (int q = 0; q < 8; ++q) {
+        const float4 t = *reinterpret_cast<const float4*>(tile + MxTile<float>::at(r, 32 * b + 4 * q));
+        v.v[4 * q] = t.x;
+        v.v[4 * q + 1] = t.y;
+        v.v[4 * q + 2] = t.z;
+        v.v[4 * q + 3] = t.w;
+    }
+}
+__device__ __forceinline__ void mx4_keep(float* tile, int r, int b, const Values<float>& v) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<float4*>(tile + MxTile<float>::at(r, 32 * b + 4 * q)) =
+            make_float4(v.v[4 * q], v.v[4 * q + 1], v.v[4 * q + 2], v.v[4 * q + 3]);
+}
+__device__ __forceinline__ void mx4_kept(const __nv_bfloat16* tile, int r, int b,
+                                         Values<__nv_bfloat16>& v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 t =
+            *reinterpret_cast<const uint4*>(tile + MxTile<__nv_bfloat16>::at(r, 32 * b + 8 * q));
+        v.w[4 * q] = t.x;
+        v.w[4 * q + 1] = t.y;
+        v.w[4 * q + 2] = t.z;
+        v.w[4 * q + 3] = t.w;
+    }
+}
+__device__ __forceinline__ void mx4_keep(__nv_bfloat16* tile, int r, int b,
+                                         const Values<__nv_bfloat16>& v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(tile + MxTile<__nv_bfloat16>::at(r, 32 * b + 8 * q)) =
+            make_uint4(v.w[4 * q], v.w[4 * q + 1], v.w[4 * q + 2], v.w[4 * q + 3]);
+}
+
+template <typename T, int FORMS, bool SR, bool VEC, bool RES>
+__global__ void __launch_bounds__(kMxThreads) k_mx4_tile(const Mx4QuantArgs a) {
+    static_assert(!RES || (FORMS == kMxRows && !VEC), "else k_mx4_rows8");
+    using V = typename std::conditional<RES, float, T>::type;   // what the tile holds
+    using S = MxTile<V>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    V* const tile = reinterpret_cast<V*>(sm);
+    uint8_t* const codes = sm + S::kBytes;            // [columns][4 blocks][16 bytes]
+    uint8_t* const exps = codes + S::kWide * 64;      // an atom, or half of one
+    uint8_t* const texps = exps + kAtomBytes;         // the transposed matrix's
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t across = a.col_tiles * S::kParts;
+    const int64_t ct = blockIdx.x % across, rt = blockIdx.x / across;
+    const int64_t r0 = rt * kAtomRows, c0 = ct * S::kWide;
+    const T* const x = static_cast<const T*>(a.x) + r0 * a.ld + c0;
+    const int rows = (int)min(a.rows - r0, (int64_t)kAtomRows);
+    const int cols = (int)max(min(a.cols - c0, (int64_t)S::kWide), (int64_t)0);
+    const int64_t pitch = mx4_pitch(a.cols);
+    const int blocks = (cols + kMxBlk - 1) / kMxBlk;
+    const auto group = [&](int r, int b) { return ((r0 + r) * pitch + c0 / 2) / 4 + b * 4; };
+    const auto row_form = [&](int r, int b, const Values<V>& v) -> uint4 {
+        uint32_t k = 0;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < rows && b < blocks) {
+            w = encode_block<SR>(v, a.key, group(r, b), k);
+            *reinterpret_cast<uint4*>(a.c + (r0 + r) * pitch + c0 / 2 + b * 16) = w;
+        }
+        exps[atom_at(r, b)] = (uint8_t)k;
+        return w;
+    };
+    if constexpr (VEC && sizeof(T) == 2) {
+        Values<T> v[2];
+        const int b = tid & 3;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = u * 64 + (tid >> 2);
+            const int n = r < rows ? min(cols - b * kMxBlk, kMxBlk) : 0;
+            const T* p = x + r * a.ld + b * kMxBlk;
+            if (n == kMxBlk)
+                v[u].load(p);
+            else
+                v[u].load_some(p, n);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = u * 64 + (tid >> 2);
+            if constexpr (FORMS & kMxColumns) mx4_keep(tile, r, b, v[u]);
+            if constexpr (FORMS & kMxRows) row_form(r, b, v[u]);
+        }
+    } else if constexpr (VEC) {
+        float v[4][8];
+        const int g = tid & 7, c = 8 * g;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = u * 32 + (tid >> 3);
+            load8(x + r * a.ld + c, (int64_t)(r < rows ? cols - c : 0), v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = u * 32 + (tid >> 3), b = g >> 2;
+            if constexpr (FORMS & kMxColumns) {
+                *reinterpret_cast<float4*>(tile + S::at(r, c)) =
+                    make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+                *reinterpret_cast<float4*>(tile + S::at(r, c + 4)) =
+                    make_float4(v[u][4], v[u][5], v[u][6], v[u][7]);
+            }
+            if constexpr (FORMS & kMxRows) {
+                uint32_t k;
+                const uint32_t w = encode_quarter<SR>(v[u], a.key, group(r, b) + (g & 3), k);
+                if (r < rows && b < blocks)
+                    *reinterpret_cast<uint32_t*>(a.c + (r0 + r) * pitch + (c0 + c) / 2) = w;
+                if ((g & 3) == 0) exps[atom_at(r, b)] = (uint8_t)k;
+            }
+        }
+    } else {
+        constexpr int kPasses = kAtomRows * S::kWide / kMxThreads, kRowParts = S::kWide / 32;
+#pragma unroll 4
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = (i / kRowParts) * kWarps + warp, c = (i % kRowParts) * 32 + lane;
+            const bool in = r < rows && c < cols;
+            V y = V(0.0f);
+            if constexpr (RES) {
+                if (in) y = __fadd_rn(ld1(x + r * a.ld + c), a.e[(r0 + r) * a.lde + c0 + c]);
+            } else {
+                if (in) y = x[r * a.ld + c];
+            }
+            tile[S::at(r, c)] = y;
+        }
+        __syncthreads();
+        if constexpr (FORMS & kMxRows) {
+            const int b = tid % S::kBlocks;
+#pragma unroll 1
+            for (int r = tid / S::kBlocks; r < kAtomRows; r += kMxThreads / S::kBlocks) {
+                Values<V> v;
+                mx4_kept(tile, r, b, v);
+                const uint4 w = row_form(r, b, v);
                 if constexpr (RES) {
-                    float q[8];
-                    decode8(w, q);
-                    const float scale = mx4_scale(k);
+                    const uint32_t scale2 = mx4_scale2(exps[atom_at(r, b)]);
+                    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) q[i] = __fsub_rn(v[u][i], q[i] * scale);
-                    if (row < a.rows) {
-                        float* er = a.e + row * a.lde;
-                        if (a.vece && col + 8 <= a.cols) {
-                            st8(er + col, q);
-                        } else {
+                    for (int g = 0; g < 4; ++g) {
+                        const uint4 q = decode8(c[g], scale2);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (col + i < a.cols) er[col + i] = q[i];
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            v.v[8 * g + i] = __fsub_rn(v.v[8 * g + i], bf16_at(q, i));
                     }
+                    mx4_keep(tile, r, b, v);
                 }
             }
         }
     }
     if constexpr (FORMS & kMxColumns) {
-        uint8_t* codes = sm + mx4_tile_bytes<T>();        // [128 columns][4 blocks][16 bytes]
-        uint8_t* exps = codes + kAtomRows * 64;           // [128 columns][4 blocks]
-        const uint32_t tkey = SR ? mx4_key(a.seed + 1) : 0u;
         const int64_t tpitch = mx4_pitch(a.rows);
-        const int64_t row_tiles = mx4_atoms(a.rows);
-        __syncthreads();
-        const auto put = [&](const float (&v)[32], int c, int b) {
-            uint32_t k;
-            const int64_t G = ((c0 + c) * tpitch + r0 / 2) / 4 + b * 4;
-            const uint4 w = encode_block<SR>(v, tkey, G, k);
-            *reinterpret_cast<uint4*>(codes + c * 64 + ((b ^ (c >> 1)) & 3) * 16) = w;
-            exps[c * 4 + b] = (uint8_t)k;
+        if constexpr (VEC) __syncthreads();
+        const int p = tid >> 6;        // the block of rows
+        const auto put = [&](auto&& get, uint32_t most, int c) {
+            const uint32_t k = mx4_exponent(most);
+            *reinterpret_cast<uint4*>(codes + c * 64 + ((p ^ (c >> 1)) & 3) * 16) =
+                encode32<SR>(get, k, a.tkey, ((c0 + c) * tpitch + r0 / 2) / 4 + p * 4);
+            texps[atom_at(c, p)] = (uint8_t)k;
         };
         if constexpr (sizeof(T) == 4) {
-            const int c = tid & 127;
-#pragma unroll 1
-            for (int b = tid >> 7; b < 4; b += 2) {
-                float v[32];
+            const int c = tid & 63;
+            Values<float> v;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = reinterpret_cast<const float*>(tile)[(b * 32 + i) * 128 + c];
-                put(v, c, b);
-            }
+            for (int i = 0; i < 32; ++i) v.v[i] = tile[S::at(p * 32 + i, c)];
+            put([&](int i) { return v.v[i]; }, v.most(), c);
         } else {
-            const int c = (tid & 63) * 2, b = tid >> 6;
-            uint32_t p[32];
+            const int c = (tid & 63) * 2;
+            uint32_t w[32];            // two columns
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                p[i] = reinterpret_cast<const uint32_t*>(tile)[(b * 32 + i) * 64 + (tid & 63)];
-            float v[32];
+                w[i] = *reinterpret_cast<const uint32_t*>(tile + S::at(p * 32 + i, c));
+            uint32_t m[2] = {w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(p[i] << 16);
-            put(v, c, b);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(p[i] & 0xffff0000u);
-            put(v, c + 1, b);
+            for (int i = 2; i < 32; ++i) m[i & 1] = max_u16x2(m[i & 1], w[i] & 0x7fff7fffu);
+            const uint32_t most = max_u16x2(m[0], m[1]);
+            put([&](int i) { return __uint_as_float(w[i] << 16); }, most << 16, c);
+            put([&](int i) { return __uint_as_float(w[i] & 0xffff0000u); }, most & 0xffff0000u, c + 1);
         }
         __syncthreads();
 #pragma unroll
-        for (int i = tid; i < kAtomCols * 4; i += kMxThreads) {
-            const int c = i >> 2, b = i & 3;
-            const int64_t at = r0 / 2 + b * 16;
-            if (c0 + c < a.cols && at < tpitch)
+        for (int i = tid; i < S::kWide * 4; i += kMxThreads) {
+            const int c = i >> 2, q = i & 3;
+            const int64_t at = r0 / 2 + q * 16;
+            if (c < cols && at < tpitch)
                 *reinterpret_cast<uint4*>(a.ct + (c0 + c) * tpitch + at) =
-                    *reinterpret_cast<const uint4*>(codes + c * 64 + ((b ^ (c >> 1)) & 3) * 16);
+                    *reinterpret_cast<const uint4*>(codes + c * 64 + ((q ^ (c >> 1)) & 3) * 16);
         }
-        if (tid < kAtomCols)
-            *reinterpret_cast<uint32_t*>(a.st + (ct * row_tiles + rt) * kAtomBytes + atom_at(tid, 0)) =
-                *reinterpret_cast<const uint32_t*>(exps + tid * 4);
+        if (tid < 32) {                // 16 or 8 of an atom's rows of 16 bytes
+            uint8_t* to = a.st + ((c0 >> 7) * mx4_atoms(a.rows) + rt) * kAtomBytes + tid * 16;
+            const uint8_t* from = texps + tid * 16;
+            if constexpr (S::kParts == 1)
+                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+            else
+                *reinterpret_cast<uint2*>(to + (ct & 1) * 8) = *reinterpret_cast<const uint2*>(from);
+        }
+    } else {
+        __syncthreads();
+    }
+    if constexpr (FORMS & kMxRows) {
+        uint8_t* to = a.s + (rt * a.col_tiles + ct / S::kParts) * kAtomBytes;
+        if constexpr (S::kParts == 1) {
+            if (tid >= 32 && tid < 64)
+                reinterpret_cast<uint4*>(to)[tid - 32] = reinterpret_cast<const uint4*>(exps)[tid - 32];
+        } else {
+            if (tid >= 128)
+                *reinterpret_cast<uint16_t*>(to + atom_at(tid - 128, (int)(ct & 1) * 2)) =
+                    *reinterpret_cast<const uint16_t*>(exps + atom_at(tid - 128, 0));
+        }
+    }
+    if constexpr (RES) {
+        constexpr int kPasses = kAtomRows * S::kWide / kMxThreads, kRowParts = S::kWide / 32;
+#pragma unroll 4
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = (i / kRowParts) * kWarps + warp, c = (i % kRowParts) * 32 + lane;
+            if (r < rows && c < cols) a.e[(r0 + r) * a.lde + c0 + c] = tile[S::at(r, c)];
+        }
     }
 }
 
@@ -326,34 +631,117 @@ struct Mx4DequantArgs {
     const uint8_t *c, *s;
     void* out;
     int64_t ld, rows, cols, col_tiles;
-    int32_t vec;
+    int32_t segments, segment, rows_per;   // as in Mx4QuantArgs, but of the blocks that there are
+    uint32_t magic;                        // (0 for one block)
 };
 
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize(const Mx4DequantArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t ct = blockIdx.x % a.col_tiles, rt = blockIdx.x / a.col_tiles;
-    const int g = lane & 15;
-    const int64_t col = ct * kAtomCols + g * 8, pitch = mx4_pitch(a.cols);
-    if (col >= a.cols) return;
+// To fp32 whose blocks are aligned to 32 bytes: eight values a thread, contiguous in a warp (8192 x
+// 8192: 50 us; a block a thread 63).
+__global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize8(const Mx4DequantArgs a) {
+    const int blocks = (int)mx4_blocks(a.cols), g = threadIdx.x & 3;
+    const int64_t pitch = mx4_pitch(a.cols);
+    MxPlace t[kMxUnits];
+    uint32_t c[kMxUnits], k[kMxUnits];
 #pragma unroll
-    for (int it = 0; it < ROWS / 16; ++it) {
-        const int64_t row = rt * ROWS + it * 16 + warp * 2 + (lane >> 4);
-        if (row >= a.rows) continue;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.c + row * pitch + col / 2);
-        const float scale =
-            mx4_scale(a.s[((row >> 7) * a.col_tiles + ct) * kAtomBytes + atom_at((int)(row & 127), g >> 2)]);
-        float v[8];
-        decode8(w, v);
+    for (int u = 0; u < kMxUnits; ++u) {
+        t[u] = mx4_place((int)threadIdx.x / 4 + u * (kMxThreads / 4), blocks, a.segments, a.segment,
+                         a.rows_per, a.magic, a.rows);
+        c[u] = k[u] = 0;
+        if (t[u].in) {
+            c[u] = *reinterpret_cast<const uint32_t*>(a.c + t[u].row * pitch + t[u].b * 16 + g * 4);
+            k[u] = a.s[((t[u].row >> 7) * a.col_tiles + (t[u].b >> 2)) * kAtomBytes +
+                       atom_at((int)(t[u].row & 127), t[u].b & 3)];
+        }
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= scale;
-        T* out = static_cast<T*>(a.out) + row * a.ld + col;
-        if (a.vec && col + 8 <= a.cols) {
-            st8(out, v);
+    for (int u = 0; u < kMxUnits; ++u) {
+        if (!t[u].in) continue;
+        const uint4 v = decode8(c[u], mx4_scale2(k[u]));
+        const int64_t col = (int64_t)t[u].b * kMxBlk + 8 * g;
+        float* out = static_cast<float*>(a.out) + t[u].row * a.ld + col;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = bf16_at(v, i);
+        if (a.cols - col >= 8) {
+            st8(out, o);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (col + i < a.cols) st1(out + i, v[i]);
+                if (col + i < a.cols) out[i] = o[i];
+        }
+    }
+}
+
+// A thread a block. VEC (bf16): out's blocks are aligned to 32 bytes. Else the values go through shared memory
+// (a warp's 32 blocks, which may be of several rows) and out by consecutive lanes; bf16 by pairs from an
+// even address on, because stores of two bytes a lane are slow (1024 x 30522: 94 us).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize(const Mx4DequantArgs a) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blocks = (int)mx4_blocks(a.cols);
+    const MxPlace t = mx4_place(tid, blocks, a.segments, a.segment, a.rows_per, a.magic, a.rows);
+    const int64_t row = t.row;
+    const int b = t.b;
+    const bool in = t.in;
+    uint4 c = make_uint4(0, 0, 0, 0);
+    uint32_t scale2 = 0;
+    if (in) {
+        c = *reinterpret_cast<const uint4*>(a.c + row * mx4_pitch(a.cols) + b * 16);
+        scale2 = mx4_scale2(a.s[((row >> 7) * a.col_tiles + (b >> 2)) * kAtomBytes +
+                                atom_at((int)(row & 127), b & 3)]);
+    }
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint4 v[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) v[g] = decode8(w[g], scale2);
+    T* const out = static_cast<T*>(a.out) + row * a.ld + (int64_t)b * kMxBlk;
+    const int n = in ? (int)min(a.cols - (int64_t)b * kMxBlk, (int64_t)kMxBlk) : 0;
+    if (VEC && n == kMxBlk) {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2)
+            asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(v[g].x),
+                         "r"(v[g].y), "r"(v[g].z), "r"(v[g].w), "r"(v[g + 1].x), "r"(v[g + 1].y),
+                         "r"(v[g + 1].z), "r"(v[g + 1].w), "l"(out + 8 * g)
+                         : "memory");
+    } else if (VEC) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) st1(out + i, bf16_at(v[i >> 3], i & 7));
+    } else {
+        // block l of the warp: 16 words of two values, word j at l * 16 + (j ^ l % 16)
+        __shared__ uint32_t values[kWarps][32 * 16];
+        uint32_t* const mine = values[warp];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t u[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mine[lane * 16 + ((4 * g + i) ^ (lane & 15))] = u[i];
+        }
+        __syncwarp();
+        const auto value = [&](int l, int i) -> uint32_t {
+            return (mine[l * 16 + ((i >> 1) ^ (l & 15))] >> (16 * (i & 1))) & 0xffffu;
+        };
+        const uint64_t at = reinterpret_cast<uint64_t>(out);
+#pragma unroll 1
+        for (int l = 0; l < 32; l += 2) {
+            // two blocks at a time: half a warp each
+            const int from = l + (lane >> 4), half = lane & 15;
+            const uint64_t p = __shfl_sync(kFull, at, from);
+            const int m = __shfl_sync(kFull, n, from);
+            if constexpr (sizeof(T) == 4) {
+                float* o = reinterpret_cast<float*>(p);
+#pragma unroll
+                for (int i = half; i < 32; i += 16)
+                    if (i < m) o[i] = __uint_as_float(value(from, i) << 16);
+            } else {
+                uint16_t* o = reinterpret_cast<uint16_t*>(p);
+                const int odd = (int)(p >> 1) & 1, i = 2 * half + odd;  // the pair from value i on
+                if (i + 1 < m)
+                    *reinterpret_cast<uint32_t*>(o + i) = value(from, i) | value(from, i + 1) << 16;
+                else if (i < m)
+                    o[i] = (uint16_t)value(from, i);
+                if (odd && half == 0 && m > 0) o[0] = (uint16_t)value(from, 0);
+            }
         }
     }
 }

@@ -9,6 +9,18 @@
 
 namespace {
 
+// The key of the random bits.
+uint32_t mx4_key(uint64_t seed) {
+    const auto mix = [](uint32_t x) {
+        x ^= x >> 16;
+        x *= 0x9016D2F5u;
+        x ^= x >> 15;
+        x *= 0x314549A1u;
+        return x ^ (x >> 16);
+    };
+    return mix(mix((uint32_t)seed + kGolden) ^ (uint32_t)(seed >> 32));
+}
+
 constexpr int64_t kMxMost = (int64_t)1 << 30;  // rows or columns
 
 int64_t mx4_code_bytes(int64_t rows, int64_t cols) { return rows * mx4_pitch(cols); }
@@ -60,25 +72,63 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
     return e;
 }
 
-template <typename T, int FORMS, bool SR, bool RES, int ROWS>
-int launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t st) {
-    constexpr int smem = mx4_quant_smem<T, FORMS>();
-    static std::atomic<uint64_t> done{0};
-    const auto kernel = k_mx4_quantize<T, FORMS, SR, RES, ROWS>;
-    if (smem > 48 * 1024) ONEBIT_CUDA(allow_smem(kernel, smem, done));
-    const int64_t blocks = a.col_tiles * mx4_atoms(a.rows) * (kAtomRows / ROWS);
-    kernel<<<(unsigned)blocks, kMxThreads, smem, st>>>(a);
+// How thread blocks of `threads` share rows of `wide` blocks: several rows each, or parts of one.
+template <typename A>
+int64_t mx4_share(A& a, int64_t rows, int64_t wide, int threads) {
+    if (wide <= threads) {
+        a.segments = 1;
+        a.segment = 0;
+        a.rows_per = (int32_t)(threads / wide);
+        a.magic = wide > 1 ? (uint32_t)(((uint64_t)1 << 32) / (uint64_t)wide + 1) : 0;
+        return ceil_div(rows, a.rows_per);
+    }
+    a.segments = (int32_t)ceil_div(wide, threads);
+    a.segment = (int32_t)ceil_div(wide, a.segments);
+    a.rows_per = 0;
+    a.magic = 0;
+    return rows * a.segments;
+}
+
+template <typename T, bool SR, bool RES>
+int launch_mx4_rows(Mx4QuantArgs a, cudaStream_t st) {
+    const int64_t rows = mx4_atoms(a.rows) * kAtomRows, wide = a.col_tiles * 4;
+    if constexpr (sizeof(T) == 2 && !RES) {
+        const int64_t blocks = mx4_share(a, rows, wide, kMxThreads);
+        k_mx4_rows<SR><<<(unsigned)blocks, kMxThreads, 0, st>>>(a);
+    } else {
+        const int64_t blocks = mx4_share(a, rows, wide, kMxThreads / 4 * kMxUnits);
+        k_mx4_rows8<T, SR, RES><<<(unsigned)blocks, kMxThreads, 0, st>>>(a);
+    }
     ONEBIT_CUDA(cudaGetLastError());
     return ONEBIT_OK;
 }
 
+template <typename T, int FORMS, bool SR, bool VEC, bool RES>
+int launch_mx4_tile(const Mx4QuantArgs& a, cudaStream_t st) {
+    using S = MxTile<typename std::conditional<RES, float, T>::type>;
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = k_mx4_tile<T, FORMS, SR, VEC, RES>;
+    ONEBIT_CUDA(allow_smem(kernel, S::kSmem, done));
+    kernel<<<(unsigned)(a.col_tiles * S::kParts * mx4_atoms(a.rows)), kMxThreads, S::kSmem, st>>>(a);
+    ONEBIT_CUDA(cudaGetLastError());
+    return ONEBIT_OK;
+}
+
+// vec: blocks of x's rows (and of the residual's) are aligned to 32 bytes.
 template <typename T, bool SR>
-int queue_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t st) {
-    const bool rows = a.c != nullptr, columns = a.ct != nullptr;
-    if (rows && columns) return launch_mx4_quantize<T, kMxRows | kMxColumns, SR, false, 128>(a, st);
-    if (columns) return launch_mx4_quantize<T, kMxColumns, SR, false, 128>(a, st);
-    if (a.e != nullptr) return launch_mx4_quantize<T, kMxRows, SR, true, 32>(a, st);
-    return launch_mx4_quantize<T, kMxRows, SR, false, 32>(a, st);
+int queue_mx4_quantize(const Mx4QuantArgs& a, bool vec, cudaStream_t st) {
+    constexpr int kBoth = kMxRows | kMxColumns;
+    if (a.c != nullptr && a.ct != nullptr)
+        return vec ? launch_mx4_tile<T, kBoth, SR, true, false>(a, st)
+                   : launch_mx4_tile<T, kBoth, SR, false, false>(a, st);
+    if (a.ct != nullptr)
+        return vec ? launch_mx4_tile<T, kMxColumns, SR, true, false>(a, st)
+                   : launch_mx4_tile<T, kMxColumns, SR, false, false>(a, st);
+    if (a.e != nullptr)
+        return vec ? launch_mx4_rows<T, SR, true>(a, st)
+                   : launch_mx4_tile<T, kMxRows, SR, false, true>(a, st);
+    return vec ? launch_mx4_rows<T, SR, false>(a, st)
+               : launch_mx4_tile<T, kMxRows, SR, false, false>(a, st);
 }
 
 // cuTensorMapEncodeTiled, asked of the runtime: the library links to no driver library.
@@ -268,16 +318,18 @@ int onebit_mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype
         a.s = scales;
         a.ct = codes_t;
         a.st = scales_t;
-        a.seed = seed;
+        a.key = mx4_key(seed);
+        a.tkey = mx4_key(seed + 1);
         a.col_tiles = mx4_atoms(cols);
-        a.vec = aligned_to(x, 8 * width(dtype)) && (rows == 1 || ld % 8 == 0);
-        a.vece = aligned_to(residual, 32) && (rows == 1 || ld_residual % 8 == 0);
+        const int64_t w = width(dtype);
+        const bool vec = aligned_to(x, 32) && (rows == 1 || ld * w % 32 == 0) &&
+                         aligned_to(residual, 32) && (residual == nullptr || rows == 1 || ld_residual % 8 == 0);
         const cudaStream_t st = as_stream(stream);
         if (dtype == ONEBIT_F32)
-            return stochastic ? queue_mx4_quantize<float, true>(a, st)
-                              : queue_mx4_quantize<float, false>(a, st);
-        return stochastic ? queue_mx4_quantize<__nv_bfloat16, true>(a, st)
-                          : queue_mx4_quantize<__nv_bfloat16, false>(a, st);
+            return stochastic ? queue_mx4_quantize<float, true>(a, vec, st)
+                              : queue_mx4_quantize<float, false>(a, vec, st);
+        return stochastic ? queue_mx4_quantize<__nv_bfloat16, true>(a, vec, st)
+                          : queue_mx4_quantize<__nv_bfloat16, false>(a, vec, st);
     });
 }
 
@@ -297,14 +349,24 @@ int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, cons
         ranges.add(1, scales, mx4_scale_bytes(rows, cols), false);
         ranges.add(2, out, mx4_span(rows, cols, ld, width(dtype)), true);
         if (ranges.clash()) return bad(where, "out overlaps the codes or exponents");
-        const Mx4DequantArgs a{codes, scales, out, ld, rows, cols, mx4_atoms(cols),
-                               aligned_to(out, 8 * width(dtype)) && (rows == 1 || ld % 8 == 0)};
-        constexpr int kRows = 32;
-        const unsigned blocks = (unsigned)(a.col_tiles * ceil_div(rows, kRows));
-        if (dtype == ONEBIT_F32)
-            k_mx4_dequantize<float, kRows><<<blocks, kMxThreads, 0, as_stream(stream)>>>(a);
-        else
-            k_mx4_dequantize<__nv_bfloat16, kRows><<<blocks, kMxThreads, 0, as_stream(stream)>>>(a);
+        Mx4DequantArgs a{};
+        a.c = codes;
+        a.s = scales;
+        a.out = out;
+        a.ld = ld;
+        a.rows = rows;
+        a.cols = cols;
+        a.col_tiles = mx4_atoms(cols);
+        const int64_t w = width(dtype);
+        const bool vec = aligned_to(out, 32) && (rows == 1 || ld * w % 32 == 0);
+        const bool wide = dtype == ONEBIT_F32;
+        const unsigned grid = (unsigned)mx4_share(
+            a, rows, mx4_blocks(cols), wide && vec ? kMxThreads / 4 * kMxUnits : kMxThreads);
+        const cudaStream_t st = as_stream(stream);
+        if (wide && vec) k_mx4_dequantize8<<<grid, kMxThreads, 0, st>>>(a);
+        else if (wide) k_mx4_dequantize<float, false><<<grid, kMxThreads, 0, st>>>(a);
+        else if (vec) k_mx4_dequantize<__nv_bfloat16, true><<<grid, kMxThreads, 0, st>>>(a);
+        else k_mx4_dequantize<__nv_bfloat16, false><<<grid, kMxThreads, 0, st>>>(a);
         ONEBIT_CUDA(cudaGetLastError());
         return ONEBIT_OK;
     });
