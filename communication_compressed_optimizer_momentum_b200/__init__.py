@@ -588,5 +588,5 @@ from .adamw import (  # noqa: E402
     ADAMW_BLOCK, AdamW, onebit_adamw8_get_state, onebit_adamw8_set_state, onebit_adamw8_step,
     onebit_adamw_layout, onebit_adamw_step, onebit_grad_norm)
 from .mx4 import (  # noqa: E402
-    MX4_BLOCK, Mx4, Mx4Linear, onebit_mx4_dequantize, onebit_mx4_layout, onebit_mx4_matmul,
-    onebit_mx4_quantize, onebit_mx4_status)
+    MX4_BLOCK, Mx4, Mx4Linear, onebit_mx4_dequantize, onebit_mx4_layout, onebit_mx4_linear,
+    onebit_mx4_linear_needs, onebit_mx4_matmul, onebit_mx4_quantize, onebit_mx4_status)

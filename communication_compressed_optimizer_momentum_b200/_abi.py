@@ -78,6 +78,8 @@ SIGNATURES = {
     "onebit_mx4_quantize": (INT, [I64, I64, P, I32, I64, P, P, P, P, I32, U64, P, I64, P]),
     "onebit_mx4_dequantize": (INT, [I64, I64, P, P, P, I32, I64, P]),
     "onebit_mx4_matmul": (INT, [I64, I64, I64, P, P, P, P, P, I32, I64, I32, P]),
+    "onebit_mx4_linear": (INT, [I64, I64, I64, P, I32, I64, P, P, P, P, P, P, P, I32, I64, P]),
+    "onebit_mx4_linear_needs": (INT, [I64, I64, I64]),
     "onebit_mx4_status": (INT, [U32P, P]),
     "onebit_strerror": (ctypes.c_char_p, [I32]),
     "onebit_last_error": (ctypes.c_char_p, []),

@@ -44,7 +44,8 @@ def _binding():
         names = ("onebit_adamw_step", "onebit_adamw8_step", "onebit_adamw8_get_state",
                  "onebit_adamw8_set_state", "onebit_grad_norm",
                  "onebit_internal_adamw_clipped_step", "onebit_mx4_layout", "onebit_mx4_quantize",
-                 "onebit_mx4_dequantize", "onebit_mx4_matmul")
+                 "onebit_mx4_dequantize", "onebit_mx4_matmul", "onebit_mx4_linear",
+                 "onebit_mx4_linear_needs")
         native.init({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names},
                     _ob().OneBitError)
         _native = native

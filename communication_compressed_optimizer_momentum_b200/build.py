@@ -22,7 +22,8 @@ DEPS = SOURCES + [os.path.join(SRC_DIR, "kernels.cuh"), os.path.join(SRC_DIR, "k
                   os.path.join(SRC_DIR, "kernels_zero_one.cuh"),
                   os.path.join(SRC_DIR, "kernels_adamw.cuh"), os.path.join(SRC_DIR, "adamw.cuh"),
                   os.path.join(SRC_DIR, "adamw_clip.h"), os.path.join(SRC_DIR, "host.h"),
-                  os.path.join(SRC_DIR, "kernels_mx4.cuh"), os.path.join(SRC_DIR, "mx4.cuh"),
+                  os.path.join(SRC_DIR, "kernels_mx4.cuh"),
+                  os.path.join(SRC_DIR, "kernels_mx4_matmul.cuh"), os.path.join(SRC_DIR, "mx4.cuh"),
                   os.path.join(INCLUDE, "onebit_adam.h")]
 
 # --fmad=false: no contraction of the method's fp32 multiply-adds (every fp32 operation is one

@@ -31,6 +31,8 @@ decltype(&onebit_mx4_layout) p_mx4_layout = nullptr;
 decltype(&onebit_mx4_quantize) p_mx4_quantize = nullptr;
 decltype(&onebit_mx4_dequantize) p_mx4_dequantize = nullptr;
 decltype(&onebit_mx4_matmul) p_mx4_matmul = nullptr;
+decltype(&onebit_mx4_linear) p_mx4_linear = nullptr;
+decltype(&onebit_mx4_linear_needs) p_mx4_linear_needs = nullptr;
 PyObject* g_error = nullptr;  // OneBitError
 constexpr int kScaleOffset = 12;  // of the clip factor in the norm's work, in bytes
 
@@ -50,6 +52,8 @@ void init(const py::dict& addresses, const py::object& error) {
     address(p_mx4_quantize, addresses, "onebit_mx4_quantize");
     address(p_mx4_dequantize, addresses, "onebit_mx4_dequantize");
     address(p_mx4_matmul, addresses, "onebit_mx4_matmul");
+    address(p_mx4_linear, addresses, "onebit_mx4_linear");
+    address(p_mx4_linear_needs, addresses, "onebit_mx4_linear_needs");
     g_error = error.inc_ref().ptr();
 }
 
@@ -470,28 +474,32 @@ void mx4_bytes(int64_t rows, int64_t cols, int64_t& codes, int64_t& scales) {
 }
 
 // From (codes, scales, rows, cols).
-Packed packed(const py::handle& o, const std::string& name, const c10::Device* device) {
-    const py::tuple t = py::cast<py::tuple>(o);
+Packed packed(const py::handle& o, const char* name, const c10::Device* device) {
+    if (!PyTuple_Check(o.ptr()) || PyTuple_GET_SIZE(o.ptr()) != 4)
+        throw py::type_error(std::string(name) + " must be an Mx4");
     Packed p;
-    p.rows = py::cast<int64_t>(t[2]);
-    p.cols = py::cast<int64_t>(t[3]);
+    p.rows = PyLong_AsLongLong(PyTuple_GET_ITEM(o.ptr(), 2));
+    p.cols = PyLong_AsLongLong(PyTuple_GET_ITEM(o.ptr(), 3));
+    if (PyErr_Occurred()) throw py::error_already_set();
     int64_t nc, ns;
     mx4_bytes(p.rows, p.cols, nc, ns);
-    p.codes = vector(t[0], at::kByte, nc, name + ".codes", device);
+    p.codes = vector(PyTuple_GET_ITEM(o.ptr(), 0), at::kByte, nc, name, device);
     const c10::Device d = p.codes.device();
-    p.scales = vector(t[1], at::kByte, ns, name + ".scales", &d);
+    p.scales = vector(PyTuple_GET_ITEM(o.ptr(), 1), at::kByte, ns, name, &d);
     return p;
 }
 
+at::Tensor new_bytes(const Queue& q, const at::Tensor& like, at::IntArrayRef sizes) {
+    return q.make([&] { return at::empty(sizes, like.options().dtype(at::kByte).requires_grad(false)); });
+}
 Packed new_packed(const Queue& q, const at::Tensor& like, int64_t rows, int64_t cols) {
     Packed p;
     p.rows = rows;
     p.cols = cols;
     int64_t nc, ns;
     mx4_bytes(rows, cols, nc, ns);
-    const auto opt = like.options().dtype(at::kByte).requires_grad(false);
-    p.codes = q.make([&] { return at::empty({rows, rows > 0 ? nc / rows : 0}, opt); });
-    p.scales = q.make([&] { return at::empty({ns}, opt); });
+    p.codes = new_bytes(q, like, {rows, rows > 0 ? nc / rows : 0});
+    p.scales = new_bytes(q, like, {ns});
     return p;
 }
 
@@ -619,6 +627,132 @@ at::Tensor mx4_matmul(const py::object& a_o, const py::object& b_o, const py::ob
     return t;
 }
 
+// ------------------------------------------------------------------------------------------
+// a linear layer's passes
+
+// x [..., width] as rows: how many, and how far apart.
+struct Rows {
+    const at::Tensor& t;
+    int64_t n, ld;
+    int32_t code;
+};
+Rows rows_of(const py::handle& o, int64_t width, const char* name, const c10::Device& device) {
+    const at::Tensor& t = tensor(o, name, &device);
+    const int32_t code = dtype_code(t.scalar_type(), name);
+    if (t.dim() < 1 || t.size(-1) != width) {
+        std::string shape;
+        for (const int64_t x : t.sizes()) shape += (shape.empty() ? "" : ", ") + std::to_string(x);
+        throw py::value_error(std::string(name) + " must have " + std::to_string(width) +
+                              " columns, got a shape of (" + shape + ")");
+    }
+    int64_t n = 1;
+    for (int64_t i = 0; i + 1 < t.dim(); ++i) n *= t.size(i);
+    if (t.dim() == 2) {
+        if (width > 1 && t.stride(1) != 1)
+            throw py::value_error(std::string(name) + " must have consecutive columns");
+        return {t, n, t.stride(0), code};
+    }
+    if (!t.is_contiguous())
+        throw py::value_error(std::string(name) + " must be contiguous, or a matrix");
+    return {t, n, width, code};
+}
+
+// A new result [..., width] for rows of another width.
+at::Tensor new_result(const Queue& q, const at::Tensor& x, int64_t width, at::ScalarType type) {
+    c10::SmallVector<int64_t, 6> sizes(x.sizes().begin(), x.sizes().end());
+    sizes.back() = width;
+    return q.make([&] { return at::empty(sizes, x.options().dtype(type).requires_grad(false)); });
+}
+
+bool was_queued(int rc) { return rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA; }
+
+// y = x W^T of w, the weights (codes, scales, outer, inner). keep: (y, codes, scales) of the
+// transposed x in 4 bits.
+py::object mx4_forward(const py::object& x_o, const py::object& w_o, bool keep,
+                       const py::object& dtype, const py::object& stream) {
+    const Packed w = packed(w_o, "the weights", nullptr);
+    const c10::Device device = w.codes.device();
+    const Rows x = rows_of(x_o, w.cols, "x", device);
+    const at::ScalarType type = result_type(dtype, x_o, x.t.scalar_type());
+    const int32_t code = dtype_code(type, "y");
+    const Queue q(device, stream);
+    const at::Tensor y = new_result(q, x.t, w.rows, type);
+    Packed kept;
+    if (keep) kept = new_packed(q, x.t, w.cols, x.n);
+    at::Tensor work;
+    uint8_t *codes = nullptr, *scales = nullptr;
+    if (keep || p_mx4_linear_needs(x.n, w.rows, w.cols)) {
+        int64_t nc, ns;
+        mx4_bytes(x.n, w.cols, nc, ns);
+        work = new_bytes(q, x.t, {nc + ns});
+        codes = work.data_ptr<uint8_t>();
+        scales = codes + nc;
+    }
+    const int rc = p_mx4_linear(x.n, w.rows, w.cols, x.t.data_ptr(), x.code, x.ld, w.c(), w.s(), codes,
+                                scales, kept.c(), kept.s(), y.data_ptr(), code, w.rows, q.handle());
+    if (was_queued(rc))
+        q.uses({&x.t, &w.codes, &w.scales, &y, &work, &kept.codes, &kept.scales});
+    refuse(rc, "onebit_mx4_linear");
+    if (!keep) return py::cast(y);
+    return py::make_tuple(y, kept.codes, kept.scales);
+}
+
+// (dx, dW) of dy: dx with the transposed weights wt (or None), dW with what forward kept (or None),
+// into grad if that is given.
+py::tuple mx4_backward(const py::object& dy_o, const py::object& wt_o, const py::object& kept_o,
+                       int64_t outer, int64_t inner, const py::object& seed, const py::object& grad,
+                       bool accumulate, const py::object& dtype, const py::object& stream) {
+    const bool to_x = !wt_o.is_none(), to_w = !kept_o.is_none();
+    const c10::Device device = tensor(dy_o, "dy", nullptr).device();
+    Packed wt, kept;
+    if (to_x) wt = packed(wt_o, "the weights", &device);
+    if (to_w) kept = packed(kept_o, "kept", &device);
+    const Rows dy = rows_of(dy_o, outer, "dy", device);
+    if (to_w && (kept.rows != inner || kept.cols != dy.n))
+        throw py::value_error("kept is " + std::to_string(kept.rows) + " x " + std::to_string(kept.cols) +
+                              ", expected " + std::to_string(inner) + " x " + std::to_string(dy.n));
+    const at::ScalarType xt = result_type(dtype, dy_o, dy.t.scalar_type());
+    const at::ScalarType gt = result_type(py::none(), grad, at::kFloat);
+    const int32_t xcode = dtype_code(xt, "dx"), gcode = dtype_code(gt, "grad");
+    const uint64_t key = PyLong_AsUnsignedLongLongMask(seed.ptr());
+    if (PyErr_Occurred()) throw py::error_already_set();
+    const Queue q(device, stream);
+    at::Tensor dx, dw;
+    if (to_w) dw = result(grad, q, kept.codes, outer, inner, gt);
+    if (to_x) dx = new_result(q, dy.t, inner, xt);
+    // dy in 4 bits, along its rows and along its columns, in one piece of memory
+    int64_t nc = 0, ns = 0, tc = 0, ts = 0;
+    if (to_x) mx4_bytes(dy.n, outer, nc, ns);
+    if (to_w) mx4_bytes(outer, dy.n, tc, ts);
+    const at::Tensor work = new_bytes(q, dy.t, {nc + ns + tc + ts});
+    uint8_t* const base = work.data_ptr<uint8_t>();
+    uint8_t* const c = to_x ? base : nullptr;
+    uint8_t* const ct = to_w ? base + nc + ns : nullptr;
+    const char* where = "onebit_mx4_quantize";
+    bool queued = false;
+    int rc = p_mx4_quantize(dy.n, outer, dy.t.data_ptr(), dy.code, dy.ld, c, c ? c + nc : nullptr, ct,
+                            ct ? ct + tc : nullptr, 1, key, nullptr, 0, q.handle());
+    queued = was_queued(rc);
+    if (rc == ONEBIT_OK && to_x) {
+        where = "onebit_mx4_matmul";
+        rc = p_mx4_matmul(dy.n, inner, outer, c, c + nc, wt.c(), wt.s(), dx.data_ptr(), xcode, inner, 0,
+                          q.handle());
+    }
+    if (rc == ONEBIT_OK && to_w) {
+        where = "onebit_mx4_matmul";
+        rc = p_mx4_matmul(outer, inner, dy.n, ct, ct + tc, kept.c(), kept.s(), dw.data_ptr(), gcode,
+                          dw.stride(0), accumulate ? 1 : 0, q.handle());
+        if (was_queued(rc)) changed({&dw});
+    }
+    if (queued)
+        q.uses({&dy.t, &wt.codes, &wt.scales, &kept.codes, &kept.scales, &work, &dx, &dw});
+    refuse(rc, where);
+    const auto or_none = [](const at::Tensor& t) {
+        return t.defined() ? py::cast(t) : py::object(py::none());
+    };
+    return py::make_tuple(or_none(dx), or_none(dw));
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_binding, m) {
@@ -630,4 +764,6 @@ PYBIND11_MODULE(_binding, m) {
     m.def("mx4_quantize", &mx4_quantize);
     m.def("mx4_dequantize", &mx4_dequantize);
     m.def("mx4_matmul", &mx4_matmul);
+    m.def("mx4_forward", &mx4_forward);
+    m.def("mx4_backward", &mx4_backward);
 }

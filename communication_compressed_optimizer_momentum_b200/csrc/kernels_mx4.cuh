@@ -1,5 +1,5 @@
-// kernels_mx4.cuh -- matrices in microscaled 4-bit floating point for B200 (sm_100a): quantising,
-// reading back, and the product of two of them on the tensor cores.
+// kernels_mx4.cuh -- matrices in microscaled 4-bit floating point for B200 (sm_100a): quantising and
+// reading back (kernels_mx4_matmul.cuh has the products).
 //
 // A matrix of rows x cols is held as codes (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5,
 // 2, 3, 4, 6; two a byte, the even column in the lower half, rows of 16 * ceil(cols / 32) bytes) and
@@ -13,9 +13,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "kernels.cuh"
@@ -210,6 +208,14 @@ __device__ __forceinline__ uint4 encode_block(const V& v, uint32_t key, int64_t 
     return encode32<SR>([&](int i) { return v.get(i); }, k, key, G);
 }
 
+// A byte permutation whose selectors are four bits: the upper one repeats the byte's top bit
+// (__byte_perm leaves it out).
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
 // Eight codes (a word) as bf16 values times a power of two: both bytes of a magnitude come from a
 // table of eight, the signs go on top. Exact: bf16 holds every such value.
 __device__ __forceinline__ uint4 decode8(uint32_t c, uint32_t scale2) {
@@ -217,8 +223,8 @@ __device__ __forceinline__ uint4 decode8(uint32_t c, uint32_t scale2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t x = h == 0 ? c : c >> 16, sel = x & 0x7777u;
-        const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, sel);
-        const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, sel);
+        const uint32_t hi = prmt(0x3f3f3f00u, 0x40404040u, sel);
+        const uint32_t lo = prmt(0xc0800000u, 0xc0804000u, sel);
         const uint32_t even = __byte_perm(lo, hi, 0x5140) | ((x & 0x8u) << 12) | ((x & 0x80u) << 24);
         const uint32_t odd =
             __byte_perm(lo, hi, 0x7362) | ((x & 0x800u) << 4) | ((x & 0x8000u) << 16);
@@ -743,664 +749,6 @@ __global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize(const Mx4DequantA
                 if (odd && half == 0 && m > 0) o[0] = (uint16_t)value(from, 0);
             }
         }
-    }
-}
-
-// ------------------------------------------------------------------------------------------
-// the product: out[i][j] = sum_k a[i][k] b[j][k]
-//
-// One thread block takes 128 columns of out (rows of b) by TM rows of out (rows of a). b's rows are the
-// 128 lanes of the accumulator in tensor memory, so that a warp's stores of one row of out are
-// consecutive whatever its strides are, and so that few rows of a (one token) take a narrow
-// instruction rather than an empty one. A stage is 256 columns of both operands (128 bytes of a row,
-// one 128-byte swizzle atom) with their exponents, four instructions of 64 columns.
-//
-// PAIR: two thread blocks of a cluster share a tile of 256 columns by 256 rows of out: each loads its
-// 128 rows of b and half of the rows of a, and one instruction of the first block multiplies in both.
-// That halves what each reads of a.
-//
-// Warps: 0 loads (TMA), 1 issues the products, 2 to 5 write out, 6 to 9 move the exponents from shared
-// to tensor memory (each its quarter of the lanes; every quarter holds all of them). The tensor cores'
-// own copies (tcgen05.cp) wait for the products before them and hold up those behind: 75 clocks an
-// atom, six for every four products (8192^3: 358 us with them).
-
-constexpr int kMmThreads = 320;
-constexpr int kMmLanes = 128;             // rows of b in a block's part of a tile
-constexpr int kStageCols = 256;
-constexpr int kExpBuffers = 4;            // stages whose exponents are in tensor memory
-constexpr uint32_t kMmTimeout = 1u;
-constexpr int kOutBytes = 2048;           // written out at a time: 32 columns of out by 32 rows (bf16)
-constexpr int kOutRows32 = 16;            // ... or by 16 (fp32)
-
-__device__ uint32_t g_mx4_status;
-
-template <int TM, bool PAIR, bool SPLIT>
-struct MmTile {
-    static constexpr int kGroup = PAIR ? 2 : 1;
-    static constexpr int kARows = TM / kGroup;                // rows of a that a block loads
-    static constexpr int kHalves = TM > 128 ? 2 : 1;          // atoms of a's exponents across
-    static constexpr int kB = kMmLanes * 128, kA = kARows * 128;  // bytes of codes in a stage
-    static constexpr int kSB = 2 * kAtomBytes, kSA = 2 * kHalves * kAtomBytes;
-    static constexpr int kStage = kB + kA + kSB + kSA;
-    // Behind the stages: what is written out (two buffers for each of four warps), or the sums of a
-    // split tile from the other blocks, [block][its rows][128].
-    static constexpr int kParts = SPLIT ? (TM + 8) * kMmLanes * 4 : 4 * 2 * kOutBytes;
-    static constexpr int kBarriers = 512;
-    static constexpr int kMost = (227 * 1024 - kBarriers - kParts) / kStage;
-    static constexpr int kStages = kMost < 8 ? kMost : 8;
-    static constexpr int kSmem = kStages * kStage + kParts + kBarriers;
-    static_assert(kStages >= kExpBuffers, "the exponents' buffers are freed with the stages");
-    // Tensor memory: two accumulators and the exponents. Two of 256 columns leave no room: they
-    // overlap by 96 columns, which are read first.
-    static constexpr int kOverlap = TM == 256 ? 96 : 0;
-    static constexpr int kSecond = TM - kOverlap;
-    static constexpr int kExp = kSecond + TM;
-    static constexpr int kExpCols = 8 + 8 * kHalves;
-    static constexpr int kNeed = kExp + kExpBuffers * kExpCols;
-    static constexpr int kColumns = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
-    static_assert(kNeed <= 512, "tensor memory");
-    static constexpr int kChunk = TM < 32 ? TM : 32;          // columns taken out at a time
-};
-
-struct Mx4Maps {
-    CUtensorMap a, b, sa, sb;  // codes and exponents
-    CUtensorMap out;           // where Mx4MatmulArgs::tma
-};
-
-struct Mx4MatmulArgs {
-    void* out;
-    int64_t ld;
-    int32_t m, n;              // rows and columns of out
-    int32_t steps;             // products of 64 columns
-    int32_t stages;            // of 256 columns
-    int32_t tiles_m, tiles_n;
-    int32_t accumulate;
-    int32_t tma;               // out's address and rows are aligned to 16 bytes
-};
-
-__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y,
-                                         uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// The barrier (of both blocks of a pair) completes when the products that this thread has issued so
-// far are done.
-template <bool PAIR>
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    if constexpr (PAIR)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-            "[%0], %1;" ::"r"(smem_addr(bar)),
-            "h"((uint16_t)3)
-            : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                     ::"r"(smem_addr(bar))
-                     : "memory");
-}
-template <bool PAIR>
-__device__ __forceinline__ void tc_product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t sa, uint32_t sb, bool add) {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-            "[%5], p;\n}\n"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-            : "memory");
-    else
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-            "[%5], p;\n}\n"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-            : "memory");
-}
-
-// Shared memory descriptor: rows of 128 bytes in 128-byte swizzle atoms of eight (1024 bytes apart).
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
-}
-
-// Both operands 4-bit (E2M1), exponents as powers of two, fp32 sums; half: which blocks of the
-// exponents' words.
-template <int TM, bool PAIR>
-__device__ __forceinline__ uint32_t product_desc(uint32_t half) {
-    return (2 * half) << 4 | 1u << 7 | 1u << 10 | (uint32_t)(TM / 8) << 17 | 1u << 23 |
-           (uint32_t)(kMmLanes * (PAIR ? 2 : 1) / 16) << 24 | (2 * half) << 29;
-}
-
-// N columns of the warp's 32 lanes, a lane each: v[j] is column j.
-template <int N>
-__device__ __forceinline__ void tc_load(uint32_t addr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    if constexpr (N == 32)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                     "%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-                     "%31}, [%32];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-                       "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                       "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-                       "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                     : "r"(addr)
-                     : "memory");
-    else
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                     "%12,%13,%14,%15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(addr)
-                     : "memory");
-}
-// N columns of 16 lanes as matrices of 8 x 8: v[4 i + 2 h + e] is lane 8 h + l / 4, column
-// 8 i + 2 (l % 4) + e in the warp's lane l.
-template <int N>
-__device__ __forceinline__ void tc_load_matrices(uint32_t addr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    if constexpr (N == 32)
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                     "%12,%13,%14,%15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(addr)
-                     : "memory");
-    else
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7])
-                     : "r"(addr)
-                     : "memory");
-}
-// What has been loaded is there (the values pass through, so that no use moves before this).
-template <int N>
-__device__ __forceinline__ void tc_load_wait(float* v) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
-}
-// Eight columns of tensor memory, a word a lane each.
-__device__ __forceinline__ void tc_store8(uint32_t addr, const uint4& a, const uint4& b) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
-                 "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-}
-
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// The address, for the cluster, of this block's `addr` in the block `rank`.
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
-    uint32_t p;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
-    return p;
-}
-__device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// Arrive on a barrier of a pair's first block. What the arrival announces are finished copies (TMA) and
-// stores to tensor memory, which the tensor cores of the arriving block's own SM read, and no plain
-// stores: the arrival needs no fence of the cluster's scope (with one, 8192^3 takes 423 us, without
-// 240).
-template <bool PAIR>
-__device__ __forceinline__ void pair_arrive(uint64_t* bar) {
-    if constexpr (PAIR)
-        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
-                         cluster_addr(smem_addr(bar), 0))
-                     : "memory");
-    else
-        mbar_arrive(bar);
-}
-// One lane of a warp that runs together: the compiler keeps what such a branch's instructions take in
-// uniform registers, which a branch on the lane's number does not let it (see k_mx4_matmul).
-__device__ __forceinline__ bool elect() {
-    uint32_t yes;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(yes));
-    return yes != 0;
-}
-
-// What a warp writes out: buffers in shared memory, and where they go.
-struct OutWarp {
-    const CUtensorMap* map;
-    uint8_t* buf;              // two of kOutBytes
-    int n0;                    // the warp's first column of out
-    int lane;
-    int count;                 // buffers filled
-};
-
-// The next buffer, once the copy out of it is over.
-__device__ __forceinline__ uint8_t* out_buffer(OutWarp& w) {
-    if (w.lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    __syncwarp();
-    return w.buf + (w.count++ & 1) * kOutBytes;
-}
-// Copy a buffer out, its first row being `row`; the map leaves out what lies behind the edges.
-__device__ __forceinline__ void out_copy(const OutWarp& w, const uint8_t* buf, int row) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (w.lane == 0) {
-        asm volatile(
-            "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(w.map),
-            "r"(w.n0), "r"(row), "r"(smem_addr(buf))
-            : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-}
-
-// A chunk of N columns of the accumulator, from tensor memory to registers. bf16: as matrices, which
-// stmatrix transposes on their way to shared memory.
-template <int N, typename OT>
-__device__ __forceinline__ void take_chunk(uint32_t addr, float* v) {
-    if constexpr (sizeof(OT) == 4) {
-        tc_load<N>(addr, v);
-    } else {
-        tc_load_matrices<N>(addr, v);
-        tc_load_matrices<N>(addr + (16u << 16), v + N / 2);
-    }
-}
-
-// Write a chunk out: rows row .. row + N - 1 of out, of which `rows` (or more) are there. The values
-// go through shared memory and by TMA, which wants aligned rows; else element by element. (bf16 from
-// 1600 columns, 8192 x 6400: two bytes a lane by plain stores 145 us; lanes exchanging values until
-// each has eight columns of a row 61.)
-template <int N, typename OT>
-__device__ __forceinline__ void put_chunk(const Mx4MatmulArgs& p, OutWarp& w, float* v, int row,
-                                          int rows) {
-    const int lane = w.lane;
-    if (rows <= 0 || w.n0 >= p.n) return;
-    if constexpr (sizeof(OT) == 4) {
-        float* const out = static_cast<float*>(p.out) + (int64_t)row * p.ld + w.n0 + lane;
-        const bool in = w.n0 + lane < p.n;
-        constexpr int kB = N < kOutRows32 ? N : kOutRows32;
-#pragma unroll
-        for (int h = 0; h < N; h += kB) {
-            if (p.accumulate) {
-                float o[kB];
-#pragma unroll
-                for (int j = 0; j < kB; ++j)
-                    o[j] = in && h + j < rows ? out[(h + j) * p.ld] : 0.0f;
-#pragma unroll
-                for (int j = 0; j < kB; ++j) v[h + j] += o[j];
-            }
-            if (p.tma) {
-                if (h < rows) {
-                    uint8_t* buf = out_buffer(w);
-#pragma unroll
-                    for (int j = 0; j < kB; ++j) reinterpret_cast<float*>(buf)[j * 32 + lane] = v[h + j];
-                    out_copy(w, buf, row + h);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kB; ++j)
-                    if (in && h + j < rows) out[(h + j) * p.ld] = v[h + j];
-            }
-        }
-    } else {
-        uint8_t* buf = out_buffer(w);
-        // matrix g of a store: columns 8 g .. 8 g + 7 of out, 16 bytes of a row of 64; the 16-byte
-        // pieces of a row are swapped as the map's 64-byte swizzle has them
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-            uint32_t x[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float* q = v + (g >> 1) * (N / 2) + 4 * i + 2 * (g & 1);
-                const __nv_bfloat162 h = __floats2bfloat162_rn(q[0], q[1]);
-                x[g] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            const int r = 8 * i + (lane & 7);
-            const uint32_t at = smem_addr(buf) + r * 64 + (((lane >> 3) ^ (r >> 1)) & 3) * 16;
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                             at),
-                         "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
-                         : "memory");
-        }
-        if (p.tma) {
-            out_copy(w, buf, row);
-        } else {
-            __syncwarp();
-            uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)row * p.ld + w.n0 + lane;
-            if (w.n0 + lane < p.n)
-                for (int r = 0; r < N && r < rows; ++r)
-                    out[r * p.ld] = *reinterpret_cast<const uint16_t*>(
-                        buf + r * 64 + (((lane >> 3) ^ (r >> 1)) & 3) * 16 + (lane & 7) * 2);
-            __syncwarp();
-        }
-    }
-}
-
-// SPLIT: a cluster of thread blocks shares one tile, each with a part of the common axis; every block
-// sends its sums to the block that adds up their rows, which does so in the blocks' order. Otherwise
-// a block (or a pair) walks over tiles, and the products of one tile run while the last one is
-// written out.
-template <int TM, bool PAIR, typename OT, bool SPLIT>
-__global__ void __launch_bounds__(kMmThreads, 1)
-k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
-    static_assert(!(PAIR && SPLIT), "one or the other");
-    using S = MmTile<TM, PAIR, SPLIT>;
-    extern __shared__ __align__(1024) uint8_t mm_smem[];
-    uint8_t* const sm = mm_smem;
-    float* const parts = reinterpret_cast<float*>(sm + S::kStages * S::kStage);
-    uint64_t* const full = reinterpret_cast<uint64_t*>(sm + S::kStages * S::kStage + S::kParts);
-    uint64_t* const ready = full + S::kStages;      // ... and the exponents are in tensor memory
-    uint64_t* const empty = ready + S::kStages;
-    uint64_t* const done = empty + S::kStages;      // [2] an accumulator is complete
-    uint64_t* const drained = done + 2;             // [2] ... and read as far as the next needs
-    uint64_t* const last = drained + 2;
-    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(last + 1);
-    const int warp = (int)__shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(ready + i, 4 * S::kGroup);
-            mbar_init(empty + i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(done + i, 1);
-            mbar_init(drained + i, 4 * S::kGroup);
-        }
-        mbar_init(last, 1);
-    }
-    if (warp == 1) {
-        if constexpr (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             smem_addr(tmem_at)),
-                         "r"(S::kColumns)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             smem_addr(tmem_at)),
-                         "r"(S::kColumns)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
-        tc_fence_before();
-    }
-    __syncthreads();
-    if constexpr (PAIR || SPLIT) {
-        cluster_arrive();
-        cluster_wait();
-    }
-    tc_fence_after();
-    const uint32_t tmem = *tmem_at;
-
-    const int rank = PAIR || SPLIT ? (int)cluster_rank() : 0;
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int nsplit = SPLIT ? (int)gridDim.x / tiles : 1;
-    const int first = SPLIT ? (int)blockIdx.x / nsplit : (int)blockIdx.x / S::kGroup;
-    const int hop = SPLIT ? tiles : (int)gridDim.x / S::kGroup;
-    const int k0 = SPLIT ? (int)((int64_t)p.stages * rank / nsplit) : 0;
-    const int k1 = SPLIT ? (int)((int64_t)p.stages * (rank + 1) / nsplit) : p.stages;
-    const int bank = PAIR ? rank : 0;               // which of the tile's rows of b
-    // Bands of 16 (8) tiles along b's rows, so that the tiles that run together share their operands
-    // in L2.
-    constexpr int kBand = 16 / S::kGroup;
-    const auto place = [&](int t, int& tm, int& tn) {
-        const int band = t / (kBand * p.tiles_m);
-        const int wide = min(kBand, p.tiles_n - band * kBand);
-        const int r = t - band * kBand * p.tiles_m;
-        tm = r / wide;
-        tn = band * kBand + r % wide;
-    };
-    bool ok = true;
-
-    if (warp == 0) {
-        int stage = 0;
-        uint32_t phase = 0;
-        int64_t filled = 0;
-        for (int t = first; t < tiles && ok; t += hop) {
-            int tm, tn;
-            place(t, tm, tn);
-            const int arow = tm * TM / kAtomRows, brow = tn * S::kGroup + bank;
-            for (int k = k0; k < k1; ++k) {
-                if (!(ok = mbar_wait_bounded(empty + stage, phase ^ 1))) break;
-                uint8_t* s = sm + stage * S::kStage;
-                if (elect()) {
-                    mbar_arrive_expect_tx(full + stage, S::kStage);
-                    tma_tile(s, &maps.b, k * 128, brow * kMmLanes, full + stage);
-                    tma_tile(s + S::kB, &maps.a, k * 128, tm * TM + bank * S::kARows, full + stage);
-                    tma_tile(s + S::kB + S::kA, &maps.sb, k * 256, brow, full + stage);
-                    tma_tile(s + S::kB + S::kA + S::kSB, &maps.sa, k * 256, arow, full + stage);
-                }
-                __syncwarp();
-                ++filled;
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (!ok && lane == 0) {  // leave no copy in flight behind
-            atomicOr(&g_mx4_status, kMmTimeout);
-            for (int64_t f = filled > S::kStages ? filled - S::kStages : 0; f < filled; ++f)
-                mbar_wait_bounded(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1);
-        }
-    } else if (warp == 1 && bank == 0) {
-        int stage = 0, c = 0;
-        uint32_t phase = 0;
-        int i = 0;
-        for (int t = first; t < tiles && ok; t += hop, ++i) {
-            int tm, tn;
-            place(t, tm, tn);
-            const uint32_t d = tmem + (uint32_t)(i & 1) * S::kSecond;
-            const int before = S::kOverlap > 0 ? i - 1 : i - 2;  // the tile that has to be read first
-            if (before >= 0 &&
-                !(ok = mbar_wait_bounded(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
-                break;
-            tc_fence_after();
-            for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = mbar_wait_bounded(ready + stage, phase))) break;
-                tc_fence_after();
-                const uint32_t s = smem_addr(sm + stage * S::kStage);
-                const uint32_t eb = tmem + S::kExp + (c % kExpBuffers) * S::kExpCols, ea = eb + 8;
-                const int steps = min(4, p.steps - 4 * k);
-                if (elect()) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (q < steps)
-                            tc_product<PAIR>(d, tile_desc(s) + 2 * q, tile_desc(s + S::kB) + 2 * q,
-                                             product_desc<TM, PAIR>(q & 1), eb + 4 * (q >> 1),
-                                             ea + 4 * S::kHalves * (q >> 1), k > k0 || q > 0);
-                    tc_commit<PAIR>(empty + stage);
-                }
-                __syncwarp();
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-            if (ok && elect()) tc_commit<PAIR>(done + (i & 1));
-            __syncwarp();
-        }
-        if (!ok && lane == 0) {
-            atomicOr(&g_mx4_status, kMmTimeout);
-            tc_commit<PAIR>(last);
-            mbar_wait_bounded(last, 0);
-        }
-    } else if (warp >= 2 && warp < 6) {
-        const int quad = warp & 3;
-        OutWarp w{&maps.out, reinterpret_cast<uint8_t*>(parts) + quad * 2 * kOutBytes, 0, lane, 0};
-        int i = 0;
-        for (int t = first; t < tiles && ok; t += hop, ++i) {
-            int tm, tn;
-            place(t, tm, tn);
-            const int buf = i & 1;
-            if (!(ok = mbar_wait_bounded(done + buf, (uint32_t)(i >> 1) & 1))) break;
-            tc_fence_after();
-            const uint32_t d = tmem + buf * S::kSecond + ((uint32_t)(quad * 32) << 16);
-            const int64_t m0 = (int64_t)tm * TM;
-            const int rows = (int)min((int64_t)TM, p.m - m0);
-            w.n0 = (tn * S::kGroup + bank) * kMmLanes + quad * 32;
-            constexpr int kC = S::kChunk;
-            const auto read_done = [&] {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) pair_arrive<PAIR>(drained + buf);
-            };
-            if constexpr (SPLIT) {
-                // lane j: the block that adds row j up, and this block's place there
-                static_assert(!SPLIT || TM <= 32, "a row a lane");
-                uint32_t to_row = 0;
-                if (lane < rows) {
-                    const int to = ((lane + 1) * nsplit - 1) / rows;
-                    const int lo = rows * to / nsplit, count = rows * (to + 1) / nsplit - lo;
-                    to_row = cluster_addr(smem_addr(parts + (rank * count + lane - lo) * kMmLanes),
-                                          (uint32_t)to);
-                }
-                float v[kC];
-                __syncwarp();
-                tc_load<kC>(d, v);
-                tc_load_wait<kC>(v);
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    const uint32_t at = __shfl_sync(kFull, to_row, j);
-                    if (j < rows) cluster_store(at + (quad * 32 + lane) * 4, v[j]);
-                }
-            } else if constexpr (S::kOverlap > 0) {
-                // what the accumulators share first: the last columns of the first, the first of the
-                // second
-                constexpr int kFirst = S::kOverlap / kC, kRest = TM / kC - kFirst;
-                const int at = buf == 0 ? kRest * kC : 0, rest = buf == 0 ? 0 : S::kOverlap;
-                float v[kFirst * kC];
-                __syncwarp();
-#pragma unroll
-                for (int u = 0; u < kFirst; ++u) take_chunk<kC, OT>(d + at + u * kC, v + u * kC);
-                tc_load_wait<kFirst * kC>(v);
-                read_done();
-#pragma unroll
-                for (int u = 0; u < kFirst; ++u)
-                    put_chunk<kC, OT>(p, w, v + u * kC, (int)m0 + at + u * kC, rows - at - u * kC);
-#pragma unroll 1
-                for (int j0 = rest; j0 < rest + kRest * kC && j0 < rows; j0 += kC) {
-                    __syncwarp();
-                    take_chunk<kC, OT>(d + j0, v);
-                    tc_load_wait<kC>(v);
-                    put_chunk<kC, OT>(p, w, v, (int)m0 + j0, rows - j0);
-                }
-            } else {
-#pragma unroll 1
-                for (int j0 = 0; j0 < TM; j0 += kC) {
-                    float v[kC];
-                    __syncwarp();
-                    take_chunk<kC, OT>(d + j0, v);
-                    tc_load_wait<kC>(v);
-                    if (j0 + kC == TM) read_done();
-                    put_chunk<kC, OT>(p, w, v, (int)m0 + j0, rows - j0);
-                }
-            }
-        }
-        if (!SPLIT && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        if (!ok && lane == 0) atomicOr(&g_mx4_status, kMmTimeout);
-    } else if (warp >= 6) {
-        int stage = 0, c = 0;
-        uint32_t phase = 0;
-        for (int t = first; t < tiles && ok; t += hop) {
-            int tm, tn;
-            place(t, tm, tn);
-            // narrow tiles: the word of the tile's first rows (32 of the atom's 128 a word) comes first,
-            // since the tensor cores take exponents from even columns on only
-            const int sub = TM < kAtomRows ? tm * TM % kAtomRows / 32 : 0;
-            for (int k = k0; k < k1; ++k, ++c) {
-                // the products that read this buffer before are done, and the stage is there
-                const int b = c - kExpBuffers;
-                if (b >= 0 && !(ok = mbar_wait_bounded(empty + b % S::kStages,
-                                                       (uint32_t)(b / S::kStages) & 1)))
-                    break;
-                if (!(ok = mbar_wait_bounded(full + stage, phase))) break;
-                const uint4* e = reinterpret_cast<const uint4*>(sm + stage * S::kStage + S::kB + S::kA) +
-                                 lane;
-                const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kExp +
-                                    (c % kExpBuffers) * S::kExpCols;
-                uint4 w[2 + 2 * S::kHalves];
-#pragma unroll
-                for (int u = 0; u < 2 + 2 * S::kHalves; ++u) w[u] = e[u * (kAtomBytes / 16)];
-                if constexpr (TM < kAtomRows) {
-#pragma unroll
-                    for (int u = 2; u < 4; ++u) {
-                        const uint4 x = w[u];
-                        w[u].x = sub == 0 ? x.x : sub == 1 ? x.y : sub == 2 ? x.z : x.w;
-                        w[u].y = sub == 0 ? x.y : sub == 2 ? x.w : 0u;   // rows 32 to 63, if any
-                    }
-                }
-                __syncwarp();
-                tc_fence_after();
-                tc_store8(at, w[0], w[1]);
-                if constexpr (S::kHalves == 1) {
-                    tc_store8(at + 8, w[2], w[3]);
-                } else {  // both halves of the first 128 columns, then of the second
-                    tc_store8(at + 8, w[2], w[4]);
-                    tc_store8(at + 16, w[3], w[5]);
-                }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) pair_arrive<PAIR>(ready + stage);
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (!ok && lane == 0) atomicOr(&g_mx4_status, kMmTimeout);
-    }
-    __syncwarp();
-    if constexpr (PAIR || SPLIT) {
-        cluster_arrive();
-        cluster_wait();
-    }
-    if constexpr (SPLIT) {
-        int tm, tn;
-        place(first, tm, tn);
-        const int64_t m0 = (int64_t)tm * TM;
-        const int rows = (int)min((int64_t)TM, p.m - m0);
-        const int lo = rows * rank / nsplit, count = rows * (rank + 1) / nsplit - lo;
-        for (int x = threadIdx.x; x < count * kMmLanes; x += kMmThreads) {
-            float v = parts[x];
-            for (int r = 1; r < nsplit; ++r) v += parts[r * count * kMmLanes + x];
-            const int n = tn * kMmLanes + x % kMmLanes;
-            OT* o = static_cast<OT*>(p.out) + (m0 + lo + x / kMmLanes) * p.ld + n;
-            if (n < p.n) {
-                if (sizeof(OT) == 4 && p.accumulate) v += ld1(o);
-                st1(o, v);
-            }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) {
-        if constexpr (PAIR)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                         "r"(S::kColumns));
-        else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                         "r"(S::kColumns));
     }
 }
 

@@ -6,6 +6,7 @@
 
 #include "host.h"
 #include "kernels_mx4.cuh"
+#include "kernels_mx4_matmul.cuh"
 
 namespace {
 
@@ -232,9 +233,10 @@ int launch_mx4_matmul(MmOperands o, int split, cudaStream_t st) {
 template <typename OT>
 int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
     const int64_t tn = ceil_div(o.n, kMmLanes), stages = o.args.stages;
-    // Few rows: narrow tiles; what they leave idle takes parts of the common axis.
+    // Few rows: narrow tiles; what they leave idle takes parts of the common axis, of four stages and
+    // more (16 x 4096 from 4096: 6.7 us in four parts, 7.2 in one; from 1024: 7.1 and 4.5).
     const auto spare = [&](int tm) {
-        return (int)std::min<int64_t>(std::min<int64_t>(8, kSms / (tn * ceil_div(o.m, tm))), stages);
+        return (int)std::min<int64_t>(std::min<int64_t>(8, kSms / (tn * ceil_div(o.m, tm))), stages / 4);
     };
     if (o.m <= 16) {
         const int split = spare(16);
@@ -255,6 +257,107 @@ int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
     const int split = spare(32);
     if (split > 1) return launch_mx4_matmul<32, false, OT, true>(o, split, st);
     return launch_mx4_matmul<32, false, OT, false>(o, 1, st);
+}
+
+// At most kFewRows rows of x, which is in 4 bits (XT uint8_t) or plain.
+template <typename XT, typename OT>
+int queue_mx4_few(const Mx4FewArgs& a, cudaStream_t st) {
+    const unsigned grid = (unsigned)(4 * mx4_atoms(a.n));
+    if (a.m == 1)
+        k_mx4_few<1, XT, OT><<<grid, kMxThreads, 0, st>>>(a);
+    else if (a.m == 2)
+        k_mx4_few<2, XT, OT><<<grid, kMxThreads, 0, st>>>(a);
+    else
+        k_mx4_few<4, XT, OT><<<grid, kMxThreads, 0, st>>>(a);
+    ONEBIT_CUDA(cudaGetLastError());
+    return ONEBIT_OK;
+}
+template <typename XT>
+int queue_mx4_few(const Mx4FewArgs& a, int32_t dtype, cudaStream_t st) {
+    return dtype == ONEBIT_F32 ? queue_mx4_few<XT, float>(a, st)
+                               : queue_mx4_few<XT, __nv_bfloat16>(a, st);
+}
+
+// out, m x n with rows ld apart, of no common axis: zeros.
+int mx4_clear(void* out, int64_t m, int64_t n, int64_t ld, int64_t w, cudaStream_t st) {
+    ONEBIT_CUDA(cudaMemset2DAsync(out, (size_t)((m > 1 ? ld : n) * w), 0, (size_t)(n * w), (size_t)m, st));
+    return ONEBIT_OK;
+}
+
+// Whether few rows are multiplied without the tensor cores: where b is small (see k_mx4_few), and a
+// little longer where that saves a launch that quantises them (one token, 6400 x 1600: 4.9 us, against
+// 2.1 and 5.0).
+bool mx4_few(int64_t m, int64_t n, int64_t k, bool plain) {
+    return m <= kFewRows && n * k <= (plain ? (int64_t)3 << 22 : (int64_t)3 << 21);
+}
+
+// The product, once everything is checked (k > 0).
+int mx4_product(int64_t m, int64_t n, int64_t k, const void* a, const void* sa, const void* b,
+                const void* sb, void* out, int32_t dtype, int64_t ld, int32_t accumulate, bool few,
+                cudaStream_t st) {
+    if (few) {
+        Mx4FewArgs f{};
+        f.x = a;
+        f.xs = static_cast<const uint8_t*>(sa);
+        f.b = static_cast<const uint8_t*>(b);
+        f.sb = static_cast<const uint8_t*>(sb);
+        f.out = out;
+        f.ld = ld;
+        f.m = (int32_t)m;
+        f.n = (int32_t)n;
+        f.k = (int32_t)k;
+        f.accumulate = accumulate;
+        return queue_mx4_few<uint8_t>(f, dtype, st);
+    }
+    MmOperands o{a, sa, b, sb, m, n, k, {}};
+    o.args.out = out;
+    o.args.ld = ld;
+    o.args.m = (int32_t)m;
+    o.args.n = (int32_t)n;
+    o.args.steps = (int32_t)ceil_div(k, 64);
+    o.args.stages = (int32_t)ceil_div(k, kStageCols);
+    o.args.accumulate = accumulate;
+    o.args.tma = aligned16(out) && (m == 1 || ld * width(dtype) % 16 == 0);
+    return dtype == ONEBIT_F32 ? queue_mx4_matmul<float>(o, st)
+                               : queue_mx4_matmul<__nv_bfloat16>(o, st);
+}
+
+// Tiles are counted in 32 bits.
+int mx4_tiles(const char* where, int64_t rows, int64_t cols) {
+    return mx4_atoms(rows) * mx4_atoms(cols) > ((int64_t)1 << 29) ? bad(where, "bad size of a matrix")
+                                                                  : ONEBIT_OK;
+}
+int mx4_out_size(const char* where, int64_t m, int64_t n) {
+    return ceil_div(m, 16) * ceil_div(n, kMmLanes) > ((int64_t)1 << 30) ? bad(where, "out is too large")
+                                                                      : ONEBIT_OK;
+}
+
+int mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype,
+                 int64_t ld, uint8_t* codes, uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t,
+                 int32_t stochastic, uint64_t seed, float* residual, int64_t ld_residual,
+                 cudaStream_t st) {
+    Mx4QuantArgs a{};
+    a.x = x;
+    a.ld = ld;
+    a.rows = rows;
+    a.cols = cols;
+    a.e = residual;
+    a.lde = ld_residual;
+    a.c = codes;
+    a.s = scales;
+    a.ct = codes_t;
+    a.st = scales_t;
+    a.key = mx4_key(seed);
+    a.tkey = mx4_key(seed + 1);
+    a.col_tiles = mx4_atoms(cols);
+    const int64_t w = width(dtype);
+    const bool vec = aligned_to(x, 32) && (rows == 1 || ld * w % 32 == 0) && aligned_to(residual, 32) &&
+                     (residual == nullptr || rows == 1 || ld_residual % 8 == 0);
+    if (dtype == ONEBIT_F32)
+        return stochastic ? queue_mx4_quantize<float, true>(a, vec, st)
+                          : queue_mx4_quantize<float, false>(a, vec, st);
+    return stochastic ? queue_mx4_quantize<__nv_bfloat16, true>(a, vec, st)
+                      : queue_mx4_quantize<__nv_bfloat16, false>(a, vec, st);
 }
 
 }  // namespace
@@ -287,14 +390,14 @@ int onebit_mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype
         if (codes == nullptr && codes_t == nullptr) return bad(where, "neither codes nor codes_t");
         if (residual != nullptr && (codes == nullptr || codes_t != nullptr))
             return bad(where, "a residual goes with codes alone");
-        rc = mx4_plain(where, "x", rows, cols, x, ld, width(dtype));
+        rc = mx4_tiles(where, rows, cols);
+        if (rc == ONEBIT_OK) rc = mx4_plain(where, "x", rows, cols, x, ld, width(dtype));
         if (rc == ONEBIT_OK && codes != nullptr) rc = mx4_matrix(where, rows, cols, codes, scales);
         if (rc == ONEBIT_OK && codes_t != nullptr)
             rc = mx4_matrix(where, cols, rows, codes_t, scales_t);
         if (rc == ONEBIT_OK && residual != nullptr)
             rc = mx4_plain(where, "residual", rows, cols, residual, ld_residual, 4);
         if (rc != ONEBIT_OK) return rc;
-        if (mx4_atoms(rows) * mx4_atoms(cols) > ((int64_t)1 << 29)) return bad(where, "bad size of a matrix");
         Ranges ranges;
         ranges.add(0, x, mx4_span(rows, cols, ld, width(dtype)), false);
         if (codes != nullptr) {
@@ -307,29 +410,8 @@ int onebit_mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype
         }
         if (residual != nullptr) ranges.add(3, residual, mx4_span(rows, cols, ld_residual, 4), true);
         if (ranges.clash()) return bad(where, "what is written overlaps something else");
-        Mx4QuantArgs a{};
-        a.x = x;
-        a.ld = ld;
-        a.rows = rows;
-        a.cols = cols;
-        a.e = residual;
-        a.lde = ld_residual;
-        a.c = codes;
-        a.s = scales;
-        a.ct = codes_t;
-        a.st = scales_t;
-        a.key = mx4_key(seed);
-        a.tkey = mx4_key(seed + 1);
-        a.col_tiles = mx4_atoms(cols);
-        const int64_t w = width(dtype);
-        const bool vec = aligned_to(x, 32) && (rows == 1 || ld * w % 32 == 0) &&
-                         aligned_to(residual, 32) && (residual == nullptr || rows == 1 || ld_residual % 8 == 0);
-        const cudaStream_t st = as_stream(stream);
-        if (dtype == ONEBIT_F32)
-            return stochastic ? queue_mx4_quantize<float, true>(a, vec, st)
-                              : queue_mx4_quantize<float, false>(a, vec, st);
-        return stochastic ? queue_mx4_quantize<__nv_bfloat16, true>(a, vec, st)
-                          : queue_mx4_quantize<__nv_bfloat16, false>(a, vec, st);
+        return mx4_quantize(rows, cols, x, dtype, ld, codes, scales, codes_t, scales_t,
+                            stochastic, seed, residual, ld_residual, as_stream(stream));
     });
 }
 
@@ -343,7 +425,8 @@ int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, cons
         rc = mx4_matrix(where, rows, cols, codes, scales);
         if (rc == ONEBIT_OK) rc = mx4_plain(where, "out", rows, cols, out, ld, width(dtype));
         if (rc != ONEBIT_OK || rows == 0 || cols == 0) return rc;
-        if (mx4_atoms(rows) * mx4_atoms(cols) > ((int64_t)1 << 29)) return bad(where, "bad size of a matrix");
+        rc = mx4_tiles(where, rows, cols);
+        if (rc != ONEBIT_OK) return rc;
         Ranges ranges;
         ranges.add(0, codes, mx4_code_bytes(rows, cols), false);
         ranges.add(1, scales, mx4_scale_bytes(rows, cols), false);
@@ -387,6 +470,7 @@ int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
         rc = mx4_matrix(where, m, k, a_codes, a_scales);
         if (rc == ONEBIT_OK) rc = mx4_matrix(where, n, k, b_codes, b_scales);
         if (rc == ONEBIT_OK) rc = mx4_plain(where, "out", m, n, out, ld, width(dtype));
+        if (rc == ONEBIT_OK) rc = mx4_out_size(where, m, n);
         if (rc != ONEBIT_OK) return rc;
         Ranges ranges;
         if (k > 0) {
@@ -398,26 +482,78 @@ int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
         ranges.add(2, out, mx4_span(m, n, ld, width(dtype)), true);
         if (ranges.clash()) return bad(where, "out overlaps an operand");
         const cudaStream_t st = as_stream(stream);
-        if (k == 0) {
-            if (!accumulate)
-                ONEBIT_CUDA(cudaMemset2DAsync(out, (size_t)((m > 1 ? ld : n) * width(dtype)), 0,
-                                              (size_t)(n * width(dtype)), (size_t)m, st));
-            return ONEBIT_OK;
-        }
-        MmOperands o{a_codes, a_scales, b_codes, b_scales, m, n, k, {}};
-        o.args.out = out;
-        o.args.ld = ld;
-        o.args.m = (int32_t)m;
-        o.args.n = (int32_t)n;
-        o.args.steps = (int32_t)ceil_div(k, 64);
-        o.args.stages = (int32_t)ceil_div(k, kStageCols);
-        o.args.accumulate = accumulate;
-        o.args.tma = aligned16(out) && (m == 1 || ld * width(dtype) % 16 == 0);
-        if (ceil_div(m, 16) * ceil_div(n, kMmLanes) > (1 << 30)) return bad(where, "out is too large");
-        return dtype == ONEBIT_F32 ? queue_mx4_matmul<float>(o, st)
-                                   : queue_mx4_matmul<__nv_bfloat16>(o, st);
+        if (k == 0) return accumulate ? ONEBIT_OK : mx4_clear(out, m, n, ld, width(dtype), st);
+        return mx4_product(m, n, k, a_codes, a_scales, b_codes, b_scales, out, dtype, ld, accumulate,
+                           mx4_few(m, n, k, false), st);
     });
 }
+
+int onebit_mx4_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype, int64_t ld_x,
+                      const uint8_t* b_codes, const uint8_t* b_scales, uint8_t* a_codes,
+                      uint8_t* a_scales, uint8_t* a_codes_t, uint8_t* a_scales_t, void* out,
+                      int32_t dtype, int64_t ld, void* stream) {
+    return guarded([&]() -> int {
+        const char* where = "onebit_mx4_linear";
+        int rc = mx4_shape(where, m, k);
+        if (rc == ONEBIT_OK) rc = mx4_shape(where, n, k);
+        if (rc != ONEBIT_OK) return rc;
+        if (!known_dtype(x_dtype) || !known_dtype(dtype)) return bad(where, "unknown type");
+        const bool kept = a_codes_t != nullptr && m > 0 && k > 0;
+        const bool few = !kept && mx4_few(m, n, k, true);
+        rc = mx4_plain(where, "x", m, k, x, ld_x, width(x_dtype));
+        if (rc == ONEBIT_OK && !few) rc = mx4_matrix(where, m, k, a_codes, a_scales);
+        if (rc == ONEBIT_OK && kept) rc = mx4_matrix(where, k, m, a_codes_t, a_scales_t);
+        if (rc == ONEBIT_OK && m > 0) rc = mx4_matrix(where, n, k, b_codes, b_scales);
+        if (rc == ONEBIT_OK) rc = mx4_plain(where, "out", m, n, out, ld, width(dtype));
+        if (rc == ONEBIT_OK) rc = mx4_out_size(where, m, n);
+        if (rc == ONEBIT_OK) rc = mx4_tiles(where, m, k);
+        if (rc != ONEBIT_OK || m == 0) return rc;
+        Ranges ranges;
+        if (k > 0) {
+            ranges.add(0, x, mx4_span(m, k, ld_x, width(x_dtype)), false);
+            if (n > 0) {
+                ranges.add(1, b_codes, mx4_code_bytes(n, k), false);
+                ranges.add(1, b_scales, mx4_scale_bytes(n, k), false);
+            }
+            if (!few) {
+                ranges.add(2, a_codes, mx4_code_bytes(m, k), true);
+                ranges.add(2, a_scales, mx4_scale_bytes(m, k), true);
+            }
+            if (kept) {
+                ranges.add(2, a_codes_t, mx4_code_bytes(k, m), true);
+                ranges.add(2, a_scales_t, mx4_scale_bytes(k, m), true);
+            }
+        }
+        ranges.add(3, out, mx4_span(m, n, ld, width(dtype)), true);
+        if (ranges.clash()) return bad(where, "what is written overlaps something else");
+        const cudaStream_t st = as_stream(stream);
+        if (k == 0) return n > 0 ? mx4_clear(out, m, n, ld, width(dtype), st) : ONEBIT_OK;
+        if (few) {
+            if (n == 0) return ONEBIT_OK;
+            Mx4FewArgs f{};
+            f.x = x;
+            f.ldx = ld_x;
+            f.b = b_codes;
+            f.sb = b_scales;
+            f.out = out;
+            f.ld = ld;
+            f.m = (int32_t)m;
+            f.n = (int32_t)n;
+            f.k = (int32_t)k;
+            f.vec = aligned_to(x, 32) && (m == 1 || ld_x * width(x_dtype) % 32 == 0);
+            return x_dtype == ONEBIT_F32 ? queue_mx4_few<float>(f, dtype, st)
+                                         : queue_mx4_few<__nv_bfloat16>(f, dtype, st);
+        }
+        rc = mx4_quantize(m, k, x, x_dtype, ld_x, a_codes, a_scales, a_codes_t, a_scales_t, 0, 0,
+                          nullptr, 0, st);
+        if (rc != ONEBIT_OK || n == 0) return rc;
+        // (with the kernel that takes x as it is, the same sums)
+        return mx4_product(m, n, k, a_codes, a_scales, b_codes, b_scales, out, dtype, ld, 0,
+                           mx4_few(m, n, k, true), st);
+    });
+}
+
+int onebit_mx4_linear_needs(int64_t m, int64_t n, int64_t k) { return mx4_few(m, n, k, true) ? 0 : 1; }
 
 int onebit_mx4_status(uint32_t* flags, void* stream) {
     return guarded([&]() -> int {

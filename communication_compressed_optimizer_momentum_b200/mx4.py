@@ -121,6 +121,21 @@ def onebit_mx4_matmul(a, b, out=None, dtype=None, accumulate: bool = False, stre
     return _binding().mx4_matmul(_parts(a, "a"), _parts(b, "b"), out, dtype, accumulate, stream)
 
 
+def onebit_mx4_linear(x, w, keep: bool = False, dtype=None, stream=None):
+    """q(x) w^T for x [..., inner] (float32 or bfloat16, rounded to nearest) and an ``Mx4`` w of inner
+    columns, of ``dtype`` (x's by default). keep: the pair with x in 4 bits in blocks along its rows, as
+    ``onebit_mx4_quantize(x, forms="columns")`` gives it."""
+    if not keep:
+        return _binding().mx4_forward(x, _parts(w, "w"), False, dtype, stream)
+    y, codes, scales = _binding().mx4_forward(x, _parts(w, "w"), True, dtype, stream)
+    return y, Mx4(codes, scales, w.cols, x.shape[:-1].numel())
+
+
+def onebit_mx4_linear_needs(m: int, n: int, k: int) -> bool:
+    """Whether ``onebit_mx4_linear`` of these sizes needs memory for x in 4 bits."""
+    return bool(_abi.lib().onebit_mx4_linear_needs(m, n, k))
+
+
 def onebit_mx4_status(stream=None) -> int:
     """Not 0 if a wait within a product on the current device ever gave up. Waits for the stream."""
     from . import _stream
@@ -167,27 +182,10 @@ class Mx4Linear:
         else:
             onebit_mx4_quantize(weight.detach(), forms="both", out=(self.w, self.wt), stream=stream)
 
-    def _rows(self, x, width: int, name: str):
-        import torch
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
-        if x.dim() < 1 or x.shape[-1] != width:
-            raise ValueError("%s must have %d columns, got a shape of %s"
-                             % (name, width, tuple(x.shape)))
-        x = x.detach()
-        if x.dim() == 2:
-            return x
-        return x.view(-1, width) if x.numel() > 0 else x.reshape(x.shape[:-1].numel(), width)
-
     def forward(self, x, keep: bool = False, dtype=None, stream=None):
         """y = x W^T for x [..., inner] (float32 or bfloat16), of ``dtype`` (x's by default). keep:
         (y, kept), where kept is x in 4 bits in blocks along the tokens, what ``backward`` needs."""
-        rows = self._rows(x, self.inner, "x")
-        q = onebit_mx4_quantize(rows, forms="both" if keep else "rows", stream=stream)
-        q, kept = q if keep else (q, None)
-        y = onebit_mx4_matmul(q, self.w, dtype=x.dtype if dtype is None else dtype, stream=stream)
-        y = y.view(*x.shape[:-1], self.outer)
-        return (y, kept) if keep else y
+        return onebit_mx4_linear(x, self.w, keep, dtype, stream)
 
     def backward(self, dy, kept: Optional[Mx4] = None, seed: int = 0, grad=None,
                  accumulate: bool = False, dtype=None, need_dx: bool = True, stream=None):
@@ -197,23 +195,12 @@ class Mx4Linear:
         rounded with: another one for every call."""
         if kept is None and (grad is not None or accumulate):
             raise ValueError("grad and accumulate need what forward kept")
+        if accumulate and grad is None:
+            raise ValueError("accumulate needs grad")
         if need_dx and self.wt is None:
             raise ValueError("made without backward=True: dx needs the weights along the outer axis")
-        import torch
-        rows = self._rows(dy, self.outer, "dy")
-        if kept is not None and _parts(kept, "kept")[2:] != (self.inner, rows.shape[0]):
-            raise ValueError("kept is %s, expected %s" % (kept.shape, (self.inner, rows.shape[0])))
         if not need_dx and kept is None:
             return None, None
-        forms = "both" if need_dx and kept is not None else "rows" if need_dx else "columns"
-        q = onebit_mx4_quantize(rows, forms=forms, rounding="stochastic", seed=seed, stream=stream)
-        q, qt = q if forms == "both" else (q, q)
-        dx = dw = None
-        if need_dx:
-            dx = onebit_mx4_matmul(q, self.wt, dtype=dy.dtype if dtype is None else dtype,
-                                   stream=stream).view(*dy.shape[:-1], self.inner)
-        if kept is not None:
-            dw = onebit_mx4_matmul(qt, kept, out=grad,
-                                   dtype=torch.float32 if grad is None else None,
-                                   accumulate=accumulate, stream=stream)
-        return dx, dw
+        return _binding().mx4_backward(
+            dy, self.wt._parts() if need_dx else None, None if kept is None else _parts(kept, "kept"),
+            self.outer, self.inner, seed, grad, accumulate, dtype, stream)

@@ -743,6 +743,20 @@ int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
                       const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
                       void* out, int32_t dtype, int64_t ld, int32_t accumulate, void* stream);
 
+/*
+ * out = q(x) b^T, the forward pass of a linear layer with weights b in 4 bits: x, m x k with rows ld_x
+ * apart, fp32 or bf16 by x_dtype, is rounded to nearest as onebit_mx4_quantize does it, and multiplied.
+ * a_codes, a_scales (of an m x k matrix) receive q(x), and a_codes_t, a_scales_t (k x m; or NULL) its
+ * transpose in blocks of its own. Where onebit_mx4_linear_needs(m, n, k) is 0 (few rows and small
+ * weights) and a_codes_t is NULL, one launch does all of it, and a_codes and a_scales are neither
+ * needed nor written.
+ */
+int onebit_mx4_linear_needs(int64_t m, int64_t n, int64_t k); /* host only */
+int onebit_mx4_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype, int64_t ld_x,
+                      const uint8_t* b_codes, const uint8_t* b_scales, uint8_t* a_codes,
+                      uint8_t* a_scales, uint8_t* a_codes_t, uint8_t* a_scales_t, void* out,
+                      int32_t dtype, int64_t ld, void* stream);
+
 /* *flags (host): 1 if a wait within a product on this device ever gave up (its result is then not
  * valid), else 0. Waits for the stream. */
 int onebit_mx4_status(uint32_t* flags, void* stream);

@@ -158,7 +158,7 @@ def tolerance(a, b, k):
     return (7 * -(-k // 64) + 7) * 2.0 ** -23 * (a.abs() @ b.abs().t())
 
 
-PRODUCTS = [(1, 1, 1), (1, 128, 64), (1, 129, 65), (16, 127, 256), (17, 1, 257), (32, 256, 128),
+PRODUCTS = [(2, 33, 31), (3, 129, 8193), (4, 6000, 1000), (4, 40, 20000), (4, 9000, 1500), (1, 1, 1), (1, 128, 64), (1, 129, 65), (16, 127, 256), (17, 1, 257), (32, 256, 128),
             (33, 100, 31), (64, 130, 1000), (65, 128, 2048), (100, 1000, 96), (128, 128, 512),
             (129, 300, 320), (256, 256, 256), (257, 129, 513), (300, 2000, 160), (1000, 77, 999),
             (1, 6400, 1600), (24, 5003, 1600), (2100, 2050, 700), (513, 50, 9000), (40, 40, 20000)]
@@ -195,7 +195,7 @@ def test_product_of_small_numbers_is_exact(m, n, k):
     assert torch.equal(ob.onebit_mx4_matmul(qa, qb, dtype=F32).double(), a @ b.t())
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 70, 500), (150, 140, 3000), (260, 40000, 64)])
+@pytest.mark.parametrize("m,n,k", [(5, 300, 1000), (3, 70, 500), (150, 140, 3000), (260, 40000, 64)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_product_into_a_slice(m, n, k, dtype):
     (qa, a), (qb, b) = quantized(m, k, 5), quantized(n, k, 6)
@@ -210,7 +210,7 @@ def test_product_into_a_slice(m, n, k, dtype):
 
 def test_product_with_nan_blocks():
     """A NaN block reaches its row or column and nothing else."""
-    for m, n, k in ((5, 300, 700), (300, 200, 4000)):
+    for m, n, k in ((3, 300, 700), (5, 300, 700), (300, 200, 4000)):
         x, y = matrix(m, k, seed=1) * 2.0 ** -8, matrix(n, k, seed=2) * 2.0 ** -8
         x[m // 2, k - 1] = float("nan")
         y[n - 1, 0] = float("inf")
@@ -226,8 +226,9 @@ def test_product_with_nan_blocks():
 
 def test_extreme_scales():
     """Exponents at both ends: products are right wherever fp32 holds them."""
-    for ea, eb in ((-126, 100), (120, -120), (-60, -60), (60, 60), (-126, 0), (125, -10)):
-        x = matrix(20, 256, seed=3).clamp(-1, 1) * 2.0 ** ea
+    for (ea, eb), m in itertools.product(((-126, 100), (120, -120), (-60, -60), (60, 60), (-126, 0),
+                                          (125, -10)), (3, 20)):
+        x = matrix(m, 256, seed=3).clamp(-1, 1) * 2.0 ** ea
         y = matrix(140, 256, seed=4).clamp(-1, 1) * 2.0 ** eb
         qa, qb = ob.onebit_mx4_quantize(x), ob.onebit_mx4_quantize(y)
         a, b = (ob.onebit_mx4_dequantize(q).double() for q in (qa, qb))
@@ -361,7 +362,8 @@ def values(q):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("tokens,inner,outer", [((1,), 64, 96), ((3, 50), 200, 130), ((515,), 96, 1000)])
+@pytest.mark.parametrize("tokens,inner,outer", [((1,), 64, 96), ((4,), 2000, 5000), ((2, 2), 77, 33),
+                                                ((), 64, 40), ((3, 50), 200, 130), ((515,), 96, 1000)])
 def test_linear_passes(tokens, inner, outer, dtype):
     w = torch.randn(outer, inner, device=DEV) * 0.1
     x = torch.randn(*tokens, inner, device=DEV).to(dtype)
@@ -499,6 +501,13 @@ def test_linear_refusals():
         linear.backward(dy, x)
     with pytest.raises(ValueError, match="kept"):
         linear.backward(dy, grad=w)
+    with pytest.raises(ValueError, match="grad"):
+        linear.backward(dy, kept, accumulate=True)
+    with pytest.raises(ValueError, match="contiguous"):
+        linear.forward(torch.zeros(3, 5, 128, device=DEV)[..., :64])
+    with pytest.raises(TypeError):
+        linear.forward(x.half())
+    assert torch.equal(linear.forward(torch.cat([x, x], 1)[:, :64]), y)   # rows apart
     with pytest.raises(ValueError, match="backward=True"):
         forward_only.backward(dy)
     assert forward_only.backward(dy, kept, need_dx=False)[1].shape == (40, 64)

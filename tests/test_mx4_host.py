@@ -202,3 +202,54 @@ def test_random_bits_are_uniform_and_unrelated():
     for i in range(4):
         for j in range(i):
             assert abs((u[i] * u[j]).mean()) < 5 * sd ** 2 / n ** 0.5
+
+
+def linear(lib, **kw):
+    a = dict(m=100, n=200, k=70, x=AT["x"], xt=0, ldx=70, b=AT["b"], sb=AT["bs"], a=AT["a"], sa=AT["as"],
+             at=AT["ct"], sat=AT["st"], out=AT["out"], dtype=1, ld=200)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    rc = lib.onebit_mx4_linear(*a.values(), None)
+    return rc, lib.onebit_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,code,why", [
+    (dict(m=-1), ARG, "size"),
+    (dict(k=1 << 31), ARG, "size"),
+    (dict(xt=3), ARG, "type"),
+    (dict(dtype=-1), ARG, "type"),
+    (dict(x=None), ARG, "null x"),
+    (dict(x=AT["x"] + 2), ALIGN, "x not aligned"),
+    (dict(ldx=69), ARG, "stride of x"),
+    (dict(b=None), ARG, "null codes"),
+    (dict(sb=AT["bs"] + 4), ALIGN, "16-byte"),
+    (dict(a=None), ARG, "null codes"),
+    (dict(a=None, at=None), ARG, "null codes"),
+    (dict(m=4, a=None), ARG, "null codes"),             # with the transposed form, memory is needed
+    (dict(m=5, a=None, at=None), ARG, "null codes"),
+    (dict(sat=None), ARG, "null codes"),
+    (dict(out=None), ARG, "null out"),
+    (dict(ld=100), ARG, "stride of out"),
+    (dict(out=AT["x"]), ARG, "overlaps"),
+    (dict(a=AT["x"]), ARG, "overlaps"),
+    (dict(at=AT["a"]), ARG, "overlaps"),
+    (dict(out=AT["b"], m=4, a=None, at=None), ARG, "overlaps"),
+])
+def test_linear_refuses(lib, kw, code, why):
+    rc, text = linear(lib, **kw)
+    assert rc == code and why in text, (rc, text)
+
+
+def test_linear_needs_memory_for_many_rows_or_large_weights():
+    assert not ob.onebit_mx4_linear_needs(4, 4096, 1024)
+    assert ob.onebit_mx4_linear_needs(5, 4096, 1024)
+    assert ob.onebit_mx4_linear_needs(1, 1 << 15, 1 << 15)
+    assert linear(_abi.lib(), m=0, x=None, b=None, sb=None, a=None, at=None, out=None)[0] == 0
+
+
+def test_linear_binding_refuses_what_is_not_on_the_gpu():
+    w = ob.Mx4.empty(40, 64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ob.onebit_mx4_linear(torch.zeros(2, 64), w)
+    with pytest.raises(TypeError, match="Mx4"):
+        ob.onebit_mx4_linear(torch.zeros(2, 64), torch.zeros(40, 64))
