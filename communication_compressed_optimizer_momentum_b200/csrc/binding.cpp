@@ -461,19 +461,23 @@ const at::Tensor& plain(const py::handle& o, const std::string& name, const c10:
     return t;
 }
 
-// A matrix in 4 bits: codes and exponents of its size.
+// A matrix in 4 bits: codes and exponents of its size, in memory of their own or (scales undefined)
+// the exponents behind the codes.
 struct Packed {
     at::Tensor codes, scales;
-    int64_t rows = 0, cols = 0;
+    int64_t rows = 0, cols = 0, code_bytes = 0;
     uint8_t* c() const { return codes.defined() ? codes.data_ptr<uint8_t>() : nullptr; }
-    uint8_t* s() const { return scales.defined() ? scales.data_ptr<uint8_t>() : nullptr; }
+    uint8_t* s() const {
+        if (scales.defined()) return scales.data_ptr<uint8_t>();
+        return codes.defined() ? codes.data_ptr<uint8_t>() + code_bytes : nullptr;
+    }
 };
 
 void mx4_bytes(int64_t rows, int64_t cols, int64_t& codes, int64_t& scales) {
     refuse(p_mx4_layout(rows, cols, &codes, &scales), "onebit_mx4_layout");
 }
 
-// From (codes, scales, rows, cols).
+// From (codes, scales or None, rows, cols).
 Packed packed(const py::handle& o, const char* name, const c10::Device* device) {
     if (!PyTuple_Check(o.ptr()) || PyTuple_GET_SIZE(o.ptr()) != 4)
         throw py::type_error(std::string(name) + " must be an Mx4");
@@ -481,30 +485,33 @@ Packed packed(const py::handle& o, const char* name, const c10::Device* device) 
     p.rows = PyLong_AsLongLong(PyTuple_GET_ITEM(o.ptr(), 2));
     p.cols = PyLong_AsLongLong(PyTuple_GET_ITEM(o.ptr(), 3));
     if (PyErr_Occurred()) throw py::error_already_set();
-    int64_t nc, ns;
-    mx4_bytes(p.rows, p.cols, nc, ns);
-    p.codes = vector(PyTuple_GET_ITEM(o.ptr(), 0), at::kByte, nc, name, device);
-    const c10::Device d = p.codes.device();
-    p.scales = vector(PyTuple_GET_ITEM(o.ptr(), 1), at::kByte, ns, name, &d);
+    int64_t ns;
+    mx4_bytes(p.rows, p.cols, p.code_bytes, ns);
+    const py::handle scales = PyTuple_GET_ITEM(o.ptr(), 1);
+    p.codes = vector(PyTuple_GET_ITEM(o.ptr(), 0), at::kByte,
+                     scales.is_none() ? p.code_bytes + ns : p.code_bytes, name, device);
+    if (!scales.is_none()) {
+        const c10::Device d = p.codes.device();
+        p.scales = vector(scales, at::kByte, ns, name, &d);
+    }
     return p;
 }
 
-at::Tensor new_bytes(const Queue& q, const at::Tensor& like, at::IntArrayRef sizes) {
-    return q.make([&] { return at::empty(sizes, like.options().dtype(at::kByte).requires_grad(false)); });
+at::Tensor new_bytes(const Queue& q, const at::Tensor& like, int64_t n) {
+    return q.make([&] { return at::empty({n}, like.options().dtype(at::kByte).requires_grad(false)); });
 }
 Packed new_packed(const Queue& q, const at::Tensor& like, int64_t rows, int64_t cols) {
     Packed p;
     p.rows = rows;
     p.cols = cols;
-    int64_t nc, ns;
-    mx4_bytes(rows, cols, nc, ns);
-    p.codes = new_bytes(q, like, {rows, rows > 0 ? nc / rows : 0});
-    p.scales = new_bytes(q, like, {ns});
+    int64_t ns;
+    mx4_bytes(rows, cols, p.code_bytes, ns);
+    p.codes = new_bytes(q, like, p.code_bytes + ns);
     return p;
 }
 
 // out: None, or (codes, scales, rows, cols) of each form that is asked for, which are then written.
-// Returns (codes, scales, codes_t, scales_t), those of a form that is not asked for None.
+// Returns the two forms' new memory (codes, then scales), None for one that is given or not asked for.
 py::tuple mx4_quantize(const py::object& x_o, bool rows, bool columns, bool stochastic,
                        const py::object& seed, const py::object& residual,
                        const py::object& out_rows, const py::object& out_columns,
@@ -539,27 +546,19 @@ py::tuple mx4_quantize(const py::object& x_o, bool rows, bool columns, bool stoc
         stochastic ? 1 : 0, key, e.defined() ? e.data_ptr<float>() : nullptr,
         e.defined() ? e.stride(0) : 0, q.handle());
     if (rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA) {
-        q.uses(x);
-        q.uses(e);
-        for (const Packed& m : p) {
-            q.uses(m.codes);
-            q.uses(m.scales);
+        q.uses({&x, &e, &p[0].codes, &p[0].scales, &p[1].codes, &p[1].scales});
+        if (e.defined()) changed({&e});
+        for (int k = 0; k < 2; ++k) {
+            if (!want[k] || given[k]->is_none()) continue;
+            changed({&p[k].codes});
+            if (p[k].scales.defined()) changed({&p[k].scales});
         }
-        std::vector<const at::Tensor*> written;
-        if (e.defined()) written.push_back(&e);
-        for (const Packed& m : p)
-            if (m.codes.defined()) {
-                written.push_back(&m.codes);
-                written.push_back(&m.scales);
-            }
-        changed(written);
     }
     refuse(rc, "onebit_mx4_quantize");
-    const auto or_none = [](const at::Tensor& t) {
-        return t.defined() ? py::cast(t) : py::object(py::none());
+    const auto made = [&](int k) {
+        return want[k] && given[k]->is_none() ? py::cast(p[k].codes) : py::object(py::none());
     };
-    return py::make_tuple(or_none(p[0].codes), or_none(p[0].scales), or_none(p[1].codes),
-                          or_none(p[1].scales));
+    return py::make_tuple(made(0), made(1));
 }
 
 at::ScalarType result_type(const py::object& dtype, const py::object& out, at::ScalarType other) {
@@ -666,8 +665,8 @@ at::Tensor new_result(const Queue& q, const at::Tensor& x, int64_t width, at::Sc
 
 bool was_queued(int rc) { return rc == ONEBIT_OK || rc == ONEBIT_ERR_CUDA; }
 
-// y = x W^T of w, the weights (codes, scales, outer, inner). keep: (y, codes, scales) of the
-// transposed x in 4 bits.
+// y = x W^T of w, the weights (codes, scales, outer, inner). keep: (y, memory of the transposed x in 4
+// bits).
 py::object mx4_forward(const py::object& x_o, const py::object& w_o, bool keep,
                        const py::object& dtype, const py::object& stream) {
     const Packed w = packed(w_o, "the weights", nullptr);
@@ -684,17 +683,17 @@ py::object mx4_forward(const py::object& x_o, const py::object& w_o, bool keep,
     if (keep || p_mx4_linear_needs(x.n, w.rows, w.cols)) {
         int64_t nc, ns;
         mx4_bytes(x.n, w.cols, nc, ns);
-        work = new_bytes(q, x.t, {nc + ns});
+        work = new_bytes(q, x.t, nc + ns);
         codes = work.data_ptr<uint8_t>();
         scales = codes + nc;
     }
     const int rc = p_mx4_linear(x.n, w.rows, w.cols, x.t.data_ptr(), x.code, x.ld, w.c(), w.s(), codes,
                                 scales, kept.c(), kept.s(), y.data_ptr(), code, w.rows, q.handle());
     if (was_queued(rc))
-        q.uses({&x.t, &w.codes, &w.scales, &y, &work, &kept.codes, &kept.scales});
+        q.uses({&x.t, &w.codes, &w.scales, &y, &work, &kept.codes});
     refuse(rc, "onebit_mx4_linear");
     if (!keep) return py::cast(y);
-    return py::make_tuple(y, kept.codes, kept.scales);
+    return py::make_tuple(y, kept.codes);
 }
 
 // (dx, dW) of dy: dx with the transposed weights wt (or None), dW with what forward kept (or None),
@@ -724,7 +723,7 @@ py::tuple mx4_backward(const py::object& dy_o, const py::object& wt_o, const py:
     int64_t nc = 0, ns = 0, tc = 0, ts = 0;
     if (to_x) mx4_bytes(dy.n, outer, nc, ns);
     if (to_w) mx4_bytes(outer, dy.n, tc, ts);
-    const at::Tensor work = new_bytes(q, dy.t, {nc + ns + tc + ts});
+    const at::Tensor work = new_bytes(q, dy.t, nc + ns + tc + ts);
     uint8_t* const base = work.data_ptr<uint8_t>();
     uint8_t* const c = to_x ? base : nullptr;
     uint8_t* const ct = to_w ? base + nc + ns : nullptr;

@@ -31,6 +31,14 @@ __host__ __device__ inline int64_t mx4_blocks(int64_t cols) { return (cols + kMx
 __host__ __device__ inline int64_t mx4_pitch(int64_t cols) { return 16 * mx4_blocks(cols); }
 __host__ __device__ inline int64_t mx4_atoms(int64_t n) { return (n + kAtomCols - 1) / kAtomCols; }
 
+// These kernels are queued so that they may start before the one ahead of them in the stream has ended:
+// each first lets its own follower start likewise, and touches memory only once everything ahead is done
+// and visible. What lies between two kernels (launch, barriers, tensor memory) overlaps then.
+__device__ __forceinline__ void after_what_is_ahead() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Byte of the exponent of a row and a block within its atom.
 __device__ __forceinline__ int atom_at(int r, int b) { return (r & 31) * 16 + (r >> 5) * 4 + b; }
 
@@ -292,6 +300,7 @@ __device__ __forceinline__ MxPlace mx4_place(int slot, int wide, int32_t segment
 
 template <bool SR>
 __global__ void __launch_bounds__(kMxThreads) k_mx4_rows(const Mx4QuantArgs a) {
+    after_what_is_ahead();
     const int wide = (int)a.col_tiles * 4;          // blocks of a row, those of no column among them
     const MxPlace t = mx4_place(threadIdx.x, wide, a.segments, a.segment, a.rows_per, a.magic,
                                 mx4_atoms(a.rows) * kAtomRows);
@@ -342,6 +351,7 @@ constexpr int kMxUnits = 2;
 
 template <typename T, bool SR, bool RES>
 __global__ void __launch_bounds__(kMxThreads) k_mx4_rows8(const Mx4QuantArgs a) {
+    after_what_is_ahead();
     const int wide = (int)a.col_tiles * 4, g = threadIdx.x & 3;
     const int64_t pitch = mx4_pitch(a.cols);
     MxPlace t[kMxUnits];
@@ -452,6 +462,7 @@ __device__ __forceinline__ void mx4_keep(__nv_bfloat16* tile, int r, int b,
 template <typename T, int FORMS, bool SR, bool VEC, bool RES>
 __global__ void __launch_bounds__(kMxThreads) k_mx4_tile(const Mx4QuantArgs a) {
     static_assert(!RES || (FORMS == kMxRows && !VEC), "else k_mx4_rows8");
+    after_what_is_ahead();
     using V = typename std::conditional<RES, float, T>::type;   // what the tile holds
     using S = MxTile<V>;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -644,6 +655,7 @@ struct Mx4DequantArgs {
 // To fp32 whose blocks are aligned to 32 bytes: eight values a thread, contiguous in a warp (8192 x
 // 8192: 50 us; a block a thread 63).
 __global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize8(const Mx4DequantArgs a) {
+    after_what_is_ahead();
     const int blocks = (int)mx4_blocks(a.cols), g = threadIdx.x & 3;
     const int64_t pitch = mx4_pitch(a.cols);
     MxPlace t[kMxUnits];
@@ -679,10 +691,12 @@ __global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize8(const Mx4Dequant
 }
 
 // A thread a block. VEC (bf16): out's blocks are aligned to 32 bytes. Else the values go through shared memory
-// (a warp's 32 blocks, which may be of several rows) and out by consecutive lanes; bf16 by pairs from an
-// even address on, because stores of two bytes a lane are slow (1024 x 30522: 94 us).
+// (a warp's 32 blocks, which may be of several rows) and out by 16 bytes a lane from the first such
+// address on, because a store instruction takes as long for less (1024 x 30522 to bf16: by two bytes a
+// lane 94 us, by four 38).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize(const Mx4DequantArgs a) {
+    after_what_is_ahead();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (int)mx4_blocks(a.cols);
     const MxPlace t = mx4_place(tid, blocks, a.segments, a.segment, a.rows_per, a.magic, a.rows);
@@ -723,30 +737,52 @@ __global__ void __launch_bounds__(kMxThreads) k_mx4_dequantize(const Mx4DequantA
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine[lane * 16 + ((4 * g + i) ^ (lane & 15))] = u[i];
         }
+        // runs of blocks of one row: this lane begins one if the lane before has another row
+        const uint32_t low = (uint32_t)row;
+        const uint32_t before = __shfl_up_sync(kFull, low, 1);
+        uint32_t starts = __ballot_sync(kFull, in && (lane == 0 || before != low));
+        const uint32_t there = __ballot_sync(kFull, in);
         __syncwarp();
-        const auto value = [&](int l, int i) -> uint32_t {
-            return (mine[l * 16 + ((i >> 1) ^ (l & 15))] >> (16 * (i & 1))) & 0xffffu;
-        };
         const uint64_t at = reinterpret_cast<uint64_t>(out);
-#pragma unroll 1
-        for (int l = 0; l < 32; l += 2) {
-            // two blocks at a time: half a warp each
-            const int from = l + (lane >> 4), half = lane & 15;
-            const uint64_t p = __shfl_sync(kFull, at, from);
-            const int m = __shfl_sync(kFull, n, from);
-            if constexpr (sizeof(T) == 4) {
-                float* o = reinterpret_cast<float*>(p);
+        while (starts != 0) {
+            const int l0 = __ffs(starts) - 1;
+            starts &= starts - 1;
+            const int l1 = starts != 0 ? __ffs(starts) - 1 : 32 - __clz(there);
+            T* const o = reinterpret_cast<T*>(__shfl_sync(kFull, at, l0));
+            const int m = (l1 - 1 - l0) * kMxBlk + __shfl_sync(kFull, n, l1 - 1);   // values of the run
+            const auto word = [&](int j) { return mine[(l0 * 16 + j) ^ ((l0 + (j >> 4)) & 15)]; };
+            const auto one = [&](int i) {
+                const uint32_t x = word(i >> 1);
+                return __uint_as_float((i & 1) ? x & 0xffff0000u : x << 16);
+            };
+            // whole 16 bytes from the first such address on, and what is before and behind them
+            constexpr int kPer = 16 / (int)sizeof(T);
+            const int head = min(m, (int)((16 - (reinterpret_cast<uint64_t>(o) & 15)) & 15) / (int)sizeof(T));
+            const int whole = (m - head) / kPer;
+            for (int j = lane; j < whole; j += 32) {
+                const int i = head + j * kPer;
+                if constexpr (sizeof(T) == 4) {
+                    float4 f;
+                    f.x = one(i);
+                    f.y = one(i + 1);
+                    f.z = one(i + 2);
+                    f.w = one(i + 3);
+                    *reinterpret_cast<float4*>(o + i) = f;
+                } else {
+                    uint32_t w[5];
 #pragma unroll
-                for (int i = half; i < 32; i += 16)
-                    if (i < m) o[i] = __uint_as_float(value(from, i) << 16);
-            } else {
-                uint16_t* o = reinterpret_cast<uint16_t*>(p);
-                const int odd = (int)(p >> 1) & 1, i = 2 * half + odd;  // the pair from value i on
-                if (i + 1 < m)
-                    *reinterpret_cast<uint32_t*>(o + i) = value(from, i) | value(from, i + 1) << 16;
-                else if (i < m)
-                    o[i] = (uint16_t)value(from, i);
-                if (odd && half == 0 && m > 0) o[0] = (uint16_t)value(from, 0);
+                    for (int q = 0; q < 4; ++q) w[q] = word((i >> 1) + q);
+                    w[4] = (i & 1) ? word((i >> 1) + 4) : 0u;
+                    const int shift = (i & 1) * 16;
+                    *reinterpret_cast<uint4*>(o + i) = make_uint4(
+                        __funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                        __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
+                }
+            }
+            const int rest = m - whole * kPer;                 // values before and behind
+            if (lane < rest) {
+                const int i = lane < head ? lane : lane + whole * kPer;
+                st1(o + i, one(i));
             }
         }
     }

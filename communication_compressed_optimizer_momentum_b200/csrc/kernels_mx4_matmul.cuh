@@ -21,12 +21,14 @@ namespace onebit {
 // 128 rows of b and half of the rows of a, and one instruction of the first block multiplies in both.
 // That halves what each reads of a.
 //
-// Warps: 0 loads (TMA), 1 issues the products, 2 to 5 write out, 6 to 9 move the exponents from shared
-// to tensor memory (each its quarter of the lanes; every quarter holds all of them). The tensor cores'
+// Warps: 0 loads (TMA), 1 issues the products, 2 to 9 write out (two for each quarter of the lanes), 10
+// to 13 move the exponents from shared to tensor memory (each its quarter of the lanes; every quarter
+// holds all of them). The tensor cores'
 // own copies (tcgen05.cp) wait for the products before them and hold up those behind: 75 clocks an
 // atom, six for every four products (8192^3: 358 us with them).
 
-constexpr int kMmThreads = 320;
+constexpr int kMmThreads = 448;
+constexpr int kOutWarps = 8;              // write out
 constexpr int kMmLanes = 128;             // rows of b in a block's part of a tile
 constexpr int kStageCols = 256;
 constexpr uint32_t kMmTimeout = 1u;
@@ -43,9 +45,9 @@ struct MmTile {
     static constexpr int kB = kMmLanes * 128, kA = kARows * 128;  // bytes of codes in a stage
     static constexpr int kSB = 2 * kAtomBytes, kSA = 2 * kHalves * kAtomBytes;
     static constexpr int kStage = kB + kA + kSB + kSA;
-    // Behind the stages: what is written out (two buffers for each of four warps), or the sums of a
-    // split tile from the other blocks, [block][its rows][128].
-    static constexpr int kParts = SPLIT ? (TM + 8) * kMmLanes * 4 : 4 * 2 * kOutBytes;
+    // Behind the stages: what is written out (a buffer for each warp), or the sums of a split tile from
+    // the other blocks, [block][its rows][128].
+    static constexpr int kParts = SPLIT ? (TM + 8) * kMmLanes * 4 : kOutWarps * kOutBytes;
     static constexpr int kBarriers = 512;
     static constexpr int kMost = (227 * 1024 - kBarriers - kParts) / kStage;
     static constexpr int kStages = kMost < 8 ? kMost : 8;
@@ -62,7 +64,7 @@ struct MmTile {
     static constexpr int kNeed = kExp + kExpBuffers * kExpCols;
     static constexpr int kColumns = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     static_assert(kNeed <= 512, "tensor memory");
-    static constexpr int kChunk = TM < 32 ? TM : 32;          // columns taken out at a time
+    static constexpr int kChunk = TM <= 32 ? 16 : 32;         // columns taken out at a time
 };
 
 struct Mx4Maps {
@@ -246,30 +248,39 @@ __device__ __forceinline__ bool elect() {
     return yes != 0;
 }
 
-// What a warp writes out: buffers in shared memory, and where they go.
+// What a warp writes out: a buffer in shared memory, and where it goes.
 struct OutWarp {
     const CUtensorMap* map;
-    uint8_t* buf;              // two of kOutBytes
+    uint8_t* buf;              // kOutBytes
     int n0;                    // the warp's first column of out
     int lane;
-    int count;                 // buffers filled
 };
 
-// The next buffer, once the copy out of it is over.
-__device__ __forceinline__ uint8_t* out_buffer(OutWarp& w) {
-    if (w.lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+// The buffer, once the copy out of it is over.
+__device__ __forceinline__ uint8_t* out_buffer(const OutWarp& w) {
+    if (w.lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
-    return w.buf + (w.count++ & 1) * kOutBytes;
+    return w.buf;
 }
-// Copy a buffer out, its first row being `row`; the map leaves out what lies behind the edges.
-__device__ __forceinline__ void out_copy(const OutWarp& w, const uint8_t* buf, int row) {
+// Copy the buffer out, or add it, its first row being `row`; the map leaves out what lies behind the
+// edges. Nobody else touches these values: there is one order of adding.
+template <bool ADD>
+__device__ __forceinline__ void out_copy(const OutWarp& w, int row) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (w.lane == 0) {
-        asm volatile(
-            "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(w.map),
-            "r"(w.n0), "r"(row), "r"(smem_addr(buf))
-            : "memory");
+        if constexpr (ADD)
+            asm volatile(
+                "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], "
+                "[%3];" ::"l"(w.map),
+                "r"(w.n0), "r"(row), "r"(smem_addr(w.buf))
+                : "memory");
+        else
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                    w.map),
+                "r"(w.n0), "r"(row), "r"(smem_addr(w.buf))
+                : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
@@ -298,27 +309,26 @@ __device__ __forceinline__ void put_chunk(const Mx4MatmulArgs& p, OutWarp& w, fl
     if constexpr (sizeof(OT) == 4) {
         float* const out = static_cast<float*>(p.out) + (int64_t)row * p.ld + w.n0 + lane;
         const bool in = w.n0 + lane < p.n;
-        constexpr int kB = N < kOutRows32 ? N : kOutRows32;
-        if (p.accumulate) {
-            float o[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) o[j] = in && j < rows ? out[j * p.ld] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] += o[j];
-        }
-#pragma unroll
-        for (int h = 0; h < N; h += kB) {
+        for (int h = 0; h < N; h += kOutRows32) {
+            if (h >= rows) break;
             if (p.tma) {
-                if (h < rows) {
-                    uint8_t* buf = out_buffer(w);
+                float* buf = reinterpret_cast<float*>(out_buffer(w));
 #pragma unroll
-                    for (int j = 0; j < kB; ++j) reinterpret_cast<float*>(buf)[j * 32 + lane] = v[h + j];
-                    out_copy(w, buf, row + h);
-                }
+                for (int j = 0; j < kOutRows32; ++j) buf[j * 32 + lane] = v[h + j];
+                if (p.accumulate)
+                    out_copy<true>(w, row + h);
+                else
+                    out_copy<false>(w, row + h);
             } else {
+                float o[kOutRows32];
 #pragma unroll
-                for (int j = 0; j < kB; ++j)
-                    if (in && h + j < rows) out[(h + j) * p.ld] = v[h + j];
+                for (int j = 0; j < kOutRows32; ++j)
+                    o[j] = p.accumulate && in && h + j < rows ? out[(h + j) * p.ld] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < kOutRows32; ++j)
+                    if (in && h + j < rows)
+                        out[(h + j) * p.ld] = p.accumulate ? o[j] + v[h + j] : v[h + j];
             }
         }
     } else {
@@ -342,7 +352,7 @@ __device__ __forceinline__ void put_chunk(const Mx4MatmulArgs& p, OutWarp& w, fl
                          : "memory");
         }
         if (p.tma) {
-            out_copy(w, buf, row);
+            out_copy<false>(w, row);
         } else {
             __syncwarp();
             uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)row * p.ld + w.n0 + lane;
@@ -384,7 +394,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(done + i, 1);
-            mbar_init(drained + i, 4 * S::kGroup);
+            mbar_init(drained + i, kOutWarps * S::kGroup);
         }
         mbar_init(last, 1);
     }
@@ -411,6 +421,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
     }
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
+    after_what_is_ahead();
 
     const int rank = PAIR || SPLIT ? (int)cluster_rank() : 0;
     const int tiles = p.tiles_m * p.tiles_n;
@@ -505,9 +516,9 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             tc_commit<PAIR>(last);
             mbar_wait_bounded(last, 0);
         }
-    } else if (warp >= 2 && warp < 6) {
-        const int quad = warp & 3;
-        OutWarp w{&maps.out, reinterpret_cast<uint8_t*>(parts) + quad * 2 * kOutBytes, 0, lane, 0};
+    } else if (warp >= 2 && warp < 2 + kOutWarps) {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        OutWarp w{&maps.out, reinterpret_cast<uint8_t*>(parts) + (warp - 2) * kOutBytes, 0, lane};
         int i = 0;
         for (int t = first; t < tiles && ok; t += hop, ++i) {
             int tm, tn;
@@ -518,14 +529,6 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const int rows = (int)min((int64_t)TM, p.m - m0);
             w.n0 = (tn * S::kGroup + bank) * kMmLanes + quad * 32;
             constexpr int kC = S::kChunk;
-            if (!SPLIT && sizeof(OT) == 4 && p.accumulate && w.n0 < p.n) {
-                // what will be added to is in L2 by then
-                for (int r = lane; r < rows; r += 32) {
-                    const float* o = static_cast<const float*>(p.out) + (m0 + r) * p.ld + w.n0;
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(o));
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(o + min(31, p.n - 1 - w.n0)));
-                }
-            }
             if (!(ok = mbar_wait_bounded(done + buf, (uint32_t)(i >> 1) & 1))) break;
             tc_fence_after();
             const auto read_done = [&] {
@@ -544,50 +547,55 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                                           (uint32_t)to);
                 }
                 float v[kC];
-                __syncwarp();
-                tc_load<kC>(d, v);
-                tc_load_wait<kC>(v);
+                const int j0 = half * kC;
+                if (j0 < TM) {
+                    __syncwarp();
+                    tc_load<kC>(d + j0, v);
+                    tc_load_wait<kC>(v);
 #pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    const uint32_t at = __shfl_sync(kFull, to_row, j);
-                    if (j < rows) cluster_store(at + (quad * 32 + lane) * 4, v[j]);
+                    for (int j = 0; j < kC; ++j) {
+                        const uint32_t at = __shfl_sync(kFull, to_row, j0 + j);
+                        if (j0 + j < rows) cluster_store(at + (quad * 32 + lane) * 4, v[j]);
+                    }
                 }
             } else if constexpr (S::kOverlap > 0) {
-                // what the accumulators share first: the last columns of the first, the first of the
-                // second
-                constexpr int kFirst = S::kOverlap / kC, kRest = TM / kC - kFirst;
-                const int at = buf == 0 ? kRest * kC : 0, rest = buf == 0 ? 0 : S::kOverlap;
-                float v[kFirst * kC];
+                // what the accumulators share first: the last 96 columns of the first, the first of the
+                // second, two chunks of the three for one warp; of the other five two as well
+                static_assert(TM == 256 && S::kOverlap == 96 && kC == 32, "the warps' shares");
+                const int at = (buf == 0 ? TM - 96 : 0) + (half == 0 ? 0 : 64);
+                const int rest = (buf == 0 ? 0 : 96) + (half == 0 ? 0 : 64);
+                const int to = rest + (half == 0 ? 64 : 96);
+                float v[2 * kC];
                 __syncwarp();
-#pragma unroll
-                for (int u = 0; u < kFirst; ++u) take_chunk<kC, OT>(d + at + u * kC, v + u * kC);
-                tc_load_wait<kFirst * kC>(v);
+                take_chunk<kC, OT>(d + at, v);
+                if (half == 0) take_chunk<kC, OT>(d + at + kC, v + kC);
+                tc_load_wait<2 * kC>(v);
                 read_done();
-#pragma unroll
-                for (int u = 0; u < kFirst; ++u)
-                    put_chunk<kC, OT>(p, w, v + u * kC, (int)m0 + at + u * kC, rows - at - u * kC);
+                put_chunk<kC, OT>(p, w, v, (int)m0 + at, rows - at);
+                if (half == 0) put_chunk<kC, OT>(p, w, v + kC, (int)m0 + at + kC, rows - at - kC);
 #pragma unroll 1
-                for (int j0 = rest; j0 < rest + kRest * kC && j0 < rows; j0 += kC) {
+                for (int j0 = rest; j0 < to && j0 < rows; j0 += kC) {
                     __syncwarp();
                     take_chunk<kC, OT>(d + j0, v);
                     tc_load_wait<kC>(v);
                     put_chunk<kC, OT>(p, w, v, (int)m0 + j0, rows - j0);
                 }
             } else {
+                if (half * kC >= TM) read_done();
 #pragma unroll 1
-                for (int j0 = 0; j0 < TM; j0 += kC) {
+                for (int j0 = half * kC; j0 < TM; j0 += 2 * kC) {
                     float v[kC];
                     __syncwarp();
                     take_chunk<kC, OT>(d + j0, v);
                     tc_load_wait<kC>(v);
-                    if (j0 + kC == TM) read_done();
+                    if (j0 + 2 * kC >= TM) read_done();
                     put_chunk<kC, OT>(p, w, v, (int)m0 + j0, rows - j0);
                 }
             }
         }
         if (!SPLIT && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok && lane == 0) atomicOr(&g_mx4_status, kMmTimeout);
-    } else if (warp >= 6) {
+    } else if (warp >= 2 + kOutWarps) {
         int stage = 0, c = 0;
         uint32_t phase = 0;
         for (int t = first; t < tiles && ok; t += hop) {
@@ -719,6 +727,7 @@ __device__ __forceinline__ uint32_t unbiased4(uint32_t v) {
 template <int MT, typename XT, typename OT>
 __global__ void __launch_bounds__(kMxThreads, 2) k_mx4_few(const Mx4FewArgs p) {
     constexpr bool kPlain = sizeof(XT) > 1;
+    after_what_is_ahead();
     // a block's two halves change places in every other four blocks: eight lanes read different banks
     __shared__ uint4 xv[MT][2 * kFewBlocks];
     __shared__ float xf[MT][kFewBlocks];                // a quarter of the block's power of two

@@ -90,18 +90,37 @@ int64_t mx4_share(A& a, int64_t rows, int64_t wide, int threads) {
     return rows * a.segments;
 }
 
+// A launch that may start before the kernel ahead of it has ended (see after_what_is_ahead).
+template <typename... P, typename... A>
+int launch_mx4(void (*kernel)(P...), int64_t grid, int threads, int smem, int cluster,
+               cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    ONEBIT_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return ONEBIT_OK;
+}
+
 template <typename T, bool SR, bool RES>
 int launch_mx4_rows(Mx4QuantArgs a, cudaStream_t st) {
     const int64_t rows = mx4_atoms(a.rows) * kAtomRows, wide = a.col_tiles * 4;
     if constexpr (sizeof(T) == 2 && !RES) {
         const int64_t blocks = mx4_share(a, rows, wide, kMxThreads);
-        k_mx4_rows<SR><<<(unsigned)blocks, kMxThreads, 0, st>>>(a);
+        return launch_mx4(k_mx4_rows<SR>, blocks, kMxThreads, 0, 1, st, a);
     } else {
         const int64_t blocks = mx4_share(a, rows, wide, kMxThreads / 4 * kMxUnits);
-        k_mx4_rows8<T, SR, RES><<<(unsigned)blocks, kMxThreads, 0, st>>>(a);
+        return launch_mx4(k_mx4_rows8<T, SR, RES>, blocks, kMxThreads, 0, 1, st, a);
     }
-    ONEBIT_CUDA(cudaGetLastError());
-    return ONEBIT_OK;
 }
 
 template <typename T, int FORMS, bool SR, bool VEC, bool RES>
@@ -110,9 +129,7 @@ int launch_mx4_tile(const Mx4QuantArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const auto kernel = k_mx4_tile<T, FORMS, SR, VEC, RES>;
     ONEBIT_CUDA(allow_smem(kernel, S::kSmem, done));
-    kernel<<<(unsigned)(a.col_tiles * S::kParts * mx4_atoms(a.rows)), kMxThreads, S::kSmem, st>>>(a);
-    ONEBIT_CUDA(cudaGetLastError());
-    return ONEBIT_OK;
+    return launch_mx4(kernel, a.col_tiles * S::kParts * mx4_atoms(a.rows), kMxThreads, S::kSmem, 1, st, a);
 }
 
 // vec: blocks of x's rows (and of the residual's) are aligned to 32 bytes.
@@ -205,29 +222,16 @@ int launch_mx4_matmul(MmOperands o, int split, cudaStream_t st) {
         rc = box_map(encode, &maps.out, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                      sizeof(OT), o.args.out, o.n, o.m, o.m > 1 ? o.args.ld : round_up(o.n, 8), 32,
-                     wide ? kOutRows32 : 32,
+                     wide ? kOutRows32 : S::kChunk,
                      wide ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B);
     }
     if (rc != ONEBIT_OK) return rc;
     o.args.tiles_m = (int32_t)ceil_div(o.m, TM);
     o.args.tiles_n = (int32_t)ceil_div(o.n, kMmLanes * S::kGroup);
     const int64_t tiles = (int64_t)o.args.tiles_m * o.args.tiles_n;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split
-                                        : std::min<int64_t>(tiles, kSms / S::kGroup) * S::kGroup));
-    cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    if (PAIR || SPLIT) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)(PAIR ? 2 : split);
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    ONEBIT_CUDA(cudaLaunchKernelEx(&cfg, kernel, maps, o.args));
-    return ONEBIT_OK;
+    const int64_t grid =
+        SPLIT ? tiles * split : std::min<int64_t>(tiles, kSms / S::kGroup) * S::kGroup;
+    return launch_mx4(kernel, grid, kMmThreads, S::kSmem, PAIR ? 2 : split, st, maps, o.args);
 }
 
 template <typename OT>
@@ -262,15 +266,10 @@ int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
 // At most kFewRows rows of x, which is in 4 bits (XT uint8_t) or plain.
 template <typename XT, typename OT>
 int queue_mx4_few(const Mx4FewArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)(4 * mx4_atoms(a.n));
-    if (a.m == 1)
-        k_mx4_few<1, XT, OT><<<grid, kMxThreads, 0, st>>>(a);
-    else if (a.m == 2)
-        k_mx4_few<2, XT, OT><<<grid, kMxThreads, 0, st>>>(a);
-    else
-        k_mx4_few<4, XT, OT><<<grid, kMxThreads, 0, st>>>(a);
-    ONEBIT_CUDA(cudaGetLastError());
-    return ONEBIT_OK;
+    const auto kernel = a.m == 1   ? k_mx4_few<1, XT, OT>
+                        : a.m == 2 ? k_mx4_few<2, XT, OT>
+                                   : k_mx4_few<4, XT, OT>;
+    return launch_mx4(kernel, 4 * mx4_atoms(a.n), kMxThreads, 0, 1, st, a);
 }
 template <typename XT>
 int queue_mx4_few(const Mx4FewArgs& a, int32_t dtype, cudaStream_t st) {
@@ -443,15 +442,13 @@ int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, cons
         const int64_t w = width(dtype);
         const bool vec = aligned_to(out, 32) && (rows == 1 || ld * w % 32 == 0);
         const bool wide = dtype == ONEBIT_F32;
-        const unsigned grid = (unsigned)mx4_share(
+        const int64_t grid = mx4_share(
             a, rows, mx4_blocks(cols), wide && vec ? kMxThreads / 4 * kMxUnits : kMxThreads);
         const cudaStream_t st = as_stream(stream);
-        if (wide && vec) k_mx4_dequantize8<<<grid, kMxThreads, 0, st>>>(a);
-        else if (wide) k_mx4_dequantize<float, false><<<grid, kMxThreads, 0, st>>>(a);
-        else if (vec) k_mx4_dequantize<__nv_bfloat16, true><<<grid, kMxThreads, 0, st>>>(a);
-        else k_mx4_dequantize<__nv_bfloat16, false><<<grid, kMxThreads, 0, st>>>(a);
-        ONEBIT_CUDA(cudaGetLastError());
-        return ONEBIT_OK;
+        const auto kernel = wide ? (vec ? k_mx4_dequantize8 : k_mx4_dequantize<float, false>)
+                            : vec ? k_mx4_dequantize<__nv_bfloat16, true>
+                                  : k_mx4_dequantize<__nv_bfloat16, false>;
+        return launch_mx4(kernel, grid, kMxThreads, 0, 1, st, a);
     });
 }
 

@@ -30,21 +30,33 @@ def onebit_mx4_layout(rows: int, cols: int) -> Tuple[int, int]:
 
 
 class Mx4:
-    """A matrix of rows x cols in 4 bits: uint8 CUDA tensors of codes and scales, in the library's
-    layout. Blocks of 32 consecutive columns share an exponent."""
+    """A matrix of rows x cols in 4 bits, in the library's layout: ``codes`` and ``scales``, uint8 CUDA
+    tensors. Blocks of 32 consecutive columns share an exponent."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("_codes", "_scales", "rows", "cols")
 
     def __init__(self, codes, scales, rows: int, cols: int):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        # scales None: codes holds both, one after the other
+        self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Mx4":
         """Room for a matrix, to be an ``out``."""
         import torch
-        codes, scales = onebit_mx4_layout(rows, cols)
-        return cls(torch.empty(codes, dtype=torch.uint8, device=device),
-                   torch.empty(scales, dtype=torch.uint8, device=device), rows, cols)
+        return cls(torch.empty(sum(onebit_mx4_layout(rows, cols)), dtype=torch.uint8, device=device),
+                   None, rows, cols)
+
+    @property
+    def codes(self):
+        """[rows][bytes of a row], two codes a byte."""
+        n = onebit_mx4_layout(self.rows, self.cols)[0]
+        return self._codes.view(-1)[:n].view(self.rows, n // self.rows if self.rows else 0)
+
+    @property
+    def scales(self):
+        """The blocks' exponents, in tiles of 128 rows by four blocks."""
+        n, m = onebit_mx4_layout(self.rows, self.cols)
+        return self._codes.view(-1)[n:n + m] if self._scales is None else self._scales
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -52,10 +64,10 @@ class Mx4:
 
     @property
     def device(self):
-        return self.codes.device
+        return self._codes.device
 
     def _parts(self):
-        return self.codes, self.scales, self.rows, self.cols
+        return self._codes, self._scales, self.rows, self.cols
 
     def __repr__(self):
         return "Mx4(%d x %d, %s)" % (self.rows, self.cols, self.device)
@@ -96,16 +108,16 @@ def onebit_mx4_quantize(x, forms: str = "rows", rounding: str = "nearest", seed:
             to_rows = _parts(out, "out")
         else:
             to_columns = _parts(out, "out")
-    codes, scales, codes_t, scales_t = _binding().mx4_quantize(
-        x, rows, columns, stochastic, seed, residual, to_rows, to_columns, stream)
+    own, transposed = _binding().mx4_quantize(x, rows, columns, stochastic, seed, residual, to_rows,
+                                              to_columns, stream)
     if out is not None:
         return out
     r, c = x.shape
     if not columns:
-        return Mx4(codes, scales, r, c)
+        return Mx4(own, None, r, c)
     if not rows:
-        return Mx4(codes_t, scales_t, c, r)
-    return Mx4(codes, scales, r, c), Mx4(codes_t, scales_t, c, r)
+        return Mx4(transposed, None, c, r)
+    return Mx4(own, None, r, c), Mx4(transposed, None, c, r)
 
 
 def onebit_mx4_dequantize(q, dtype=None, out=None, stream=None):
@@ -127,8 +139,8 @@ def onebit_mx4_linear(x, w, keep: bool = False, dtype=None, stream=None):
     ``onebit_mx4_quantize(x, forms="columns")`` gives it."""
     if not keep:
         return _binding().mx4_forward(x, _parts(w, "w"), False, dtype, stream)
-    y, codes, scales = _binding().mx4_forward(x, _parts(w, "w"), True, dtype, stream)
-    return y, Mx4(codes, scales, w.cols, x.shape[:-1].numel())
+    y, kept = _binding().mx4_forward(x, _parts(w, "w"), True, dtype, stream)
+    return y, Mx4(kept, None, w.cols, x.shape[:-1].numel())
 
 
 def onebit_mx4_linear_needs(m: int, n: int, k: int) -> bool:
