@@ -178,8 +178,12 @@ class AdamW:
             if len(mx4) != len(params):
                 raise ValueError("%d mx4 entries for %d parameters" % (len(mx4), len(params)))
             for p, linear in zip(params, mx4):
-                if linear is not None:
-                    linear.check_weight(p)
+                if linear is None:
+                    continue
+                if not isinstance(linear, _ob().Mx4Linear):
+                    raise TypeError("mx4 entries must be Mx4Linear or None, got %s"
+                                    % type(linear).__name__)
+                linear.check_weight(p)
         self._step(params, grads, lr, copies, grad_scale, stream)
         for p, linear in zip(params, mx4 or ()):
             if linear is not None:

@@ -100,36 +100,39 @@ __device__ __forceinline__ uint32_t encode8_stochastic(const float (&y)[8], uint
     return r;
 }
 
-// Eight values to codes in a block of exponent k; w: the random word.
-template <bool SR>
-__device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t k, uint32_t w) {
-    float z[8];
-    uint32_t c;
-    if constexpr (SR) {
-        // one factor where fp32 has it, 2^(1 - k)
-        if (k <= 127u) {
-            const float f = k == 0u ? 2.0f : __uint_as_float((128u - k) << 23);
+// Values to codes in a block of exponent k, eight at a time: GROUPS groups; get(i): the values; word(g):
+// the random word of a group.
+template <bool SR, int GROUPS, typename F, typename W>
+__device__ __forceinline__ void encode_groups(F&& get, W&& word, uint32_t k, uint32_t (&codes)[GROUPS]) {
+    const auto all = [&](auto&& scaled) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = __fmul_rz(v[i], f);
-        } else {
-            const float inv = mx4_inverse(k);
+        for (int g = 0; g < GROUPS; ++g) {
+            float z[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = __fmul_rz(v[i] * inv, 0x1p-126f);
+            for (int i = 0; i < 8; ++i) z[i] = scaled(get(8 * g + i));
+            if constexpr (SR)
+                codes[g] = encode8_stochastic(z, word(g));
+            else
+                codes[g] = encode8_nearest(z);
+            if (k == kMxNan) codes[g] = 0u;
         }
-        c = encode8_stochastic(z, w);
+    };
+    const float inv = mx4_inverse(k);
+    if constexpr (!SR) {
+        all([&](float v) { return v * inv; });
+    } else if (k <= 127u) {            // one factor where fp32 has it, 2^(1 - k)
+        const float f = k == 0u ? 2.0f : __uint_as_float((128u - k) << 23);
+        all([&](float v) { return __fmul_rz(v, f); });
     } else {
-        const float inv = mx4_inverse(k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = v[i] * inv;
-        c = encode8_nearest(z);
+        all([&](float v) { return __fmul_rz(v * inv, 0x1p-126f); });
     }
-    return k == kMxNan ? 0u : c;
 }
 
 // Largest magnitudes by their patterns: any NaN is above infinity.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+// (bf16 pairs: the result's signs mean nothing.)
+__device__ __forceinline__ uint32_t max_magnitude2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -172,10 +175,10 @@ struct Values<__nv_bfloat16> {
         return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
     __device__ __forceinline__ uint32_t most() const {
-        uint32_t m[2] = {w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu};
+        uint32_t m[2] = {w[0], w[1]};
 #pragma unroll
-        for (int i = 2; i < 16; ++i) m[i & 1] = max_u16x2(m[i & 1], w[i] & 0x7fff7fffu);
-        const uint32_t x = max_u16x2(m[0], m[1]);
+        for (int i = 2; i < 16; ++i) m[i & 1] = max_magnitude2(m[i & 1], w[i]);
+        const uint32_t x = max_magnitude2(m[0], m[1]) & 0x7fff7fffu;
         return max(x << 16, x & 0xffff0000u);
     }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
@@ -198,15 +201,9 @@ struct Values<__nv_bfloat16> {
 // Codes of a block of exponent k; get(i): its values; G: its first place / 8; key: of the random bits.
 template <bool SR, typename F>
 __device__ __forceinline__ uint4 encode32(F&& get, uint32_t k, uint32_t key, int64_t G) {
-    const uint32_t kh = SR ? key + (uint32_t)(G >> 32) * kGolden : 0u;
+    const uint32_t kh = SR ? key + (uint32_t)(G >> 32) * kGolden + (uint32_t)G : 0u;
     uint32_t w[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = get(8 * g + i);
-        w[g] = encode8<SR>(v, k, SR ? mix32((uint32_t)G + g + kh) : 0u);
-    }
+    encode_groups<SR>(get, [&](int g) { return mix32(kh + g); }, k, w);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The same with the exponent that the block takes.
@@ -344,7 +341,9 @@ __device__ __forceinline__ uint32_t encode_quarter(const float (&v)[8], uint32_t
     most = max(most, __shfl_xor_sync(kFull, most, 1));
     most = max(most, __shfl_xor_sync(kFull, most, 2));
     k = mx4_exponent(most);
-    return encode8<SR>(v, k, SR ? group_word(key, G) : 0u);
+    uint32_t w[1];
+    encode_groups<SR>([&](int i) { return v[i]; }, [&](int) { return group_word(key, G); }, k, w);
+    return w[0];
 }
 
 constexpr int kMxUnits = 2;
@@ -593,10 +592,10 @@ __global__ void __launch_bounds__(kMxThreads) k_mx4_tile(const Mx4QuantArgs a) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 w[i] = *reinterpret_cast<const uint32_t*>(tile + S::at(p * 32 + i, c));
-            uint32_t m[2] = {w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu};
+            uint32_t m[2] = {w[0], w[1]};
 #pragma unroll
-            for (int i = 2; i < 32; ++i) m[i & 1] = max_u16x2(m[i & 1], w[i] & 0x7fff7fffu);
-            const uint32_t most = max_u16x2(m[0], m[1]);
+            for (int i = 2; i < 32; ++i) m[i & 1] = max_magnitude2(m[i & 1], w[i]);
+            const uint32_t most = max_magnitude2(m[0], m[1]) & 0x7fff7fffu;
             put([&](int i) { return __uint_as_float(w[i] << 16); }, most << 16, c);
             put([&](int i) { return __uint_as_float(w[i] & 0xffff0000u); }, most & 0xffff0000u, c + 1);
         }

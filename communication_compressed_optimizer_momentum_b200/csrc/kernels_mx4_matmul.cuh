@@ -32,10 +32,26 @@ constexpr int kOutWarps = 8;              // write out
 constexpr int kMmLanes = 128;             // rows of b in a block's part of a tile
 constexpr int kStageCols = 256;
 constexpr uint32_t kMmTimeout = 1u;
+constexpr uint64_t kMmWaitNs = 20ull * 1000 * 1000 * 1000;   // of one wait; the longest tile takes one
 constexpr int kOutBytes = 2048;           // written out at a time: 32 columns of out by 32 rows (bf16)
 constexpr int kOutRows32 = 16;            // ... or by 16 (fp32)
 
 __device__ uint32_t g_mx4_status;
+
+// Wait for phase `parity` of the barrier, giving up after kMmWaitNs (a long common axis keeps the warps
+// that write out waiting for a good while: a number of polls would not say how long).
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    uint64_t start, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
+    do {
+        for (int i = 0; i < 256; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    } while (now - start < kMmWaitNs);
+    return false;
+}
 
 template <int TM, bool PAIR, bool SPLIT>
 struct MmTile {
@@ -452,7 +468,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             place(t, tm, tn);
             const int arow = tm * TM / kAtomRows, brow = tn * S::kGroup + bank;
             for (int k = k0; k < k1; ++k) {
-                if (!(ok = mbar_wait_bounded(empty + stage, phase ^ 1))) break;
+                if (!(ok = mm_wait(empty + stage, phase ^ 1))) break;
                 uint8_t* s = sm + stage * S::kStage;
                 if (elect()) {
                     mbar_arrive_expect_tx(full + stage, S::kStage);
@@ -472,7 +488,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
         if (!ok && lane == 0) {  // leave no copy in flight behind
             atomicOr(&g_mx4_status, kMmTimeout);
             for (int64_t f = filled > S::kStages ? filled - S::kStages : 0; f < filled; ++f)
-                mbar_wait_bounded(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1);
+                mm_wait(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1);
         }
     } else if (warp == 1 && bank == 0) {
         int stage = 0, c = 0;
@@ -484,11 +500,11 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const uint32_t d = tmem + (uint32_t)(i & 1) * S::kSecond;
             const int before = S::kOverlap > 0 ? i - 1 : i - 2;  // the tile that has to be read first
             if (before >= 0 &&
-                !(ok = mbar_wait_bounded(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
+                !(ok = mm_wait(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
                 break;
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = mbar_wait_bounded(ready + stage, phase))) break;
+                if (!(ok = mm_wait(ready + stage, phase))) break;
                 tc_fence_after();
                 const uint32_t s = smem_addr(sm + stage * S::kStage);
                 const uint32_t eb = tmem + S::kExp + (c % S::kExpBuffers) * S::kExpCols, ea = eb + 8;
@@ -514,7 +530,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
         if (!ok && lane == 0) {
             atomicOr(&g_mx4_status, kMmTimeout);
             tc_commit<PAIR>(last);
-            mbar_wait_bounded(last, 0);
+            mm_wait(last, 0);
         }
     } else if (warp >= 2 && warp < 2 + kOutWarps) {
         const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -529,7 +545,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const int rows = (int)min((int64_t)TM, p.m - m0);
             w.n0 = (tn * S::kGroup + bank) * kMmLanes + quad * 32;
             constexpr int kC = S::kChunk;
-            if (!(ok = mbar_wait_bounded(done + buf, (uint32_t)(i >> 1) & 1))) break;
+            if (!(ok = mm_wait(done + buf, (uint32_t)(i >> 1) & 1))) break;
             tc_fence_after();
             const auto read_done = [&] {
                 tc_fence_before();
@@ -605,7 +621,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             // since the tensor cores take exponents from even columns on only
             const int sub = TM < kAtomRows ? tm * TM % kAtomRows / 32 : 0;
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = mbar_wait_bounded(full + stage, phase))) break;
+                if (!(ok = mm_wait(full + stage, phase))) break;
                 const uint4* e = reinterpret_cast<const uint4*>(sm + stage * S::kStage + S::kB + S::kA) +
                                  lane;
                 const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kExp +
@@ -625,7 +641,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                 // the stage itself, for which its loads have waited)
                 const int b = c - S::kExpBuffers;
                 if (S::kExpBuffers < S::kStages && b >= 0 &&
-                    !(ok = mbar_wait_bounded(empty + b % S::kStages, (uint32_t)(b / S::kStages) & 1)))
+                    !(ok = mm_wait(empty + b % S::kStages, (uint32_t)(b / S::kStages) & 1)))
                     break;
                 __syncwarp();
                 tc_fence_after();

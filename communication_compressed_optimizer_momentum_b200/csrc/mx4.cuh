@@ -316,7 +316,8 @@ int mx4_product(int64_t m, int64_t n, int64_t k, const void* a, const void* sa, 
     o.args.steps = (int32_t)ceil_div(k, 64);
     o.args.stages = (int32_t)ceil_div(k, kStageCols);
     o.args.accumulate = accumulate;
-    o.args.tma = aligned16(out) && (m == 1 || ld * width(dtype) % 16 == 0);
+    o.args.tma = aligned16(out) && (m == 1 || (ld * width(dtype) % 16 == 0 &&
+                                               ld * width(dtype) < (int64_t)1 << 40));
     return dtype == ONEBIT_F32 ? queue_mx4_matmul<float>(o, st)
                                : queue_mx4_matmul<__nv_bfloat16>(o, st);
 }

@@ -517,7 +517,7 @@ def test_linear_refusals():
         linear.update(w.cpu())
     opt = ob.AdamW([w, dy])
     before = w.clone()
-    for mx4, error in (([linear], ValueError), ([None, linear], ValueError)):
+    for mx4, error in (([linear], ValueError), ([None, linear], ValueError), ([w, None], TypeError)):
         with pytest.raises(error):
             opt.step([w, dy], [w.clone(), dy.clone()], 1e-3, mx4=mx4)
     assert torch.equal(w, before) and opt.counts() == (0, 0)
