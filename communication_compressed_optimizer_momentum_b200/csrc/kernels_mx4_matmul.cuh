@@ -23,9 +23,12 @@ namespace onebit {
 //
 // Warps: 0 loads (TMA), 1 issues the products, 2 to 9 write out (two for each quarter of the lanes), 10
 // to 13 move the exponents from shared to tensor memory (each its quarter of the lanes; every quarter
-// holds all of them). The tensor cores'
-// own copies (tcgen05.cp) wait for the products before them and hold up those behind: 75 clocks an
-// atom, six for every four products (8192^3: 358 us with them).
+// holds all of them). The tensor cores' own copies (tcgen05.cp) wait for the products before them and
+// hold up those behind: 75 clocks an atom, six for every four products.
+//
+// 8192 x 8192 x 8192 to bf16 takes 164 us, 177 in a row: the tensor pipe is busy 85% of it, at the clock
+// that the power cap leaves (1.55 GHz). Short common axes are bound by loads and results sharing the
+// path to L2 (8192 x 6400 from 1600 columns: 41 us, 30 without storing), small products by their launch.
 
 constexpr int kMmThreads = 448;
 constexpr int kOutWarps = 8;              // write out
@@ -256,7 +259,7 @@ __device__ __forceinline__ void pair_arrive(uint64_t* bar) {
         mbar_arrive(bar);
 }
 // One lane of a warp that runs together: the compiler keeps what such a branch's instructions take in
-// uniform registers, which a branch on the lane's number does not let it (see k_mx4_matmul).
+// uniform registers, which a branch on the lane's number does not let it (200 clocks a product, so 128).
 __device__ __forceinline__ bool elect() {
     uint32_t yes;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -316,7 +319,7 @@ __device__ __forceinline__ void take_chunk(uint32_t addr, float* v) {
 // Write a chunk out: rows row .. row + N - 1 of out, of which `rows` (or more) are there. The values
 // go through shared memory and by TMA, which wants aligned rows; else element by element. (bf16 from
 // 1600 columns, 8192 x 6400: two bytes a lane by plain stores 145 us; lanes exchanging values until
-// each has eight columns of a row 61.)
+// each has eight columns of a row 61; by TMA 41.)
 template <int N, typename OT>
 __device__ __forceinline__ void put_chunk(const Mx4MatmulArgs& p, OutWarp& w, float* v, int row,
                                           int rows) {

@@ -247,13 +247,17 @@ int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
         if (split > 1) return launch_mx4_matmul<16, false, OT, true>(o, split, st);
         return launch_mx4_matmul<16, false, OT, false>(o, 1, st);
     }
-    // Rounds of tiles times a tile's clocks: a stage's, measured, and its share of the writing out.
-    const auto cost = [&](int tm, int group, int64_t stage, int64_t tile) {
+    // What a launch takes, in 10 ns, as measured: once, and a round of tiles by its stages and by what
+    // it writes. (4096 x 4096 from 1024: tiles of 64 rows 14.0 us, 128 10.2, 256 10.1; 1024 x 1024 from
+    // 1024: 5.0, 5.5, 7.3; 512 x 4096 from 4096: 13.4, 8.9, 11.2.)
+    const bool wide = sizeof(OT) == 4;
+    const auto cost = [&](int tm, int group, int64_t once, int64_t stage, int64_t tile) {
         const int64_t tiles = ceil_div(o.m, tm) * ceil_div(o.n, kMmLanes * group);
-        return ceil_div(tiles, kSms / group) * (stages * stage + tile);
+        return once + ceil_div(tiles, kSms / group) * (stages * stage + tile);
     };
-    const int64_t c32 = cost(32, 1, 400, 600), c64 = cost(64, 1, 460, 900),
-                  c128 = cost(128, 1, 600, 1500), c256 = cost(256, 2, 640, 2500);
+    const int64_t c32 = cost(32, 1, 390, 20, 30), c64 = cost(64, 1, 390, 22, wide ? 60 : 40),
+                  c128 = cost(128, 1, 400, 24, wide ? 120 : 60),
+                  c256 = cost(256, 2, 590, 31, wide ? 250 : 80);
     const int64_t best = std::min(std::min(c32, c64), std::min(c128, c256));
     if (best == c256) return launch_mx4_matmul<256, true, OT, false>(o, 1, st);
     if (best == c128) return launch_mx4_matmul<128, false, OT, false>(o, 1, st);

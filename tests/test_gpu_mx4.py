@@ -316,6 +316,75 @@ def test_another_stream_and_captured_calls():
     assert torch.equal(out, want) and torch.equal(out2, want)
 
 
+def test_captured_with_a_fork_and_other_nodes_between():
+    """Launches that may begin early, after a join of two streams, a copy and a fill."""
+    x = matrix(300, 500, seed=1)
+    w = ob.onebit_mx4_quantize(matrix(200, 500, seed=2))
+    want = ob.onebit_mx4_matmul(ob.onebit_mx4_quantize(x), w)
+    buf, out, out2 = torch.zeros_like(x), torch.ones_like(want), torch.ones(300, 200, device=DEV)
+    q, q2 = ob.Mx4.empty(300, 500), ob.Mx4.empty(300, 500)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        buf.copy_(x)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            ob.onebit_mx4_quantize(buf, out=q)
+        ob.onebit_mx4_quantize(buf, out=q2)
+        here.wait_stream(side)
+        ob.onebit_mx4_matmul(q, w, out=out)
+        out2.zero_()
+        ob.onebit_mx4_matmul(q2, w, out=out2, accumulate=True)
+    for _ in range(3):
+        buf.fill_(float("nan"))
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out2.bfloat16(), want)
+
+
+def test_products_on_two_streams_at_once():
+    """Both fill the GPU, with pairs and with clusters of other sizes."""
+    shapes = [(1024, 2048, 2048), (16, 2048, 8192), (300, 4000, 1000), (4, 4096, 1024), (30, 100, 16384)]
+    data = [(quantized(m, k, 1)[0], quantized(n, k, 2)[0]) for m, n, k in shapes]
+    want = [ob.onebit_mx4_matmul(a, b, dtype=F32) for a, b in data]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                for a, b in data[::1 if i else -1]:
+                    got[i].append(ob.onebit_mx4_matmul(a, b, dtype=F32))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, x in enumerate(got[i]):
+            k = j % len(data)
+            assert torch.equal(x, want[k if i else len(data) - 1 - k])
+    assert ob.onebit_mx4_status() == 0
+
+
+def test_a_chain_of_short_calls():
+    """Each reads what the one before wrote, many times over: none starts too early. (The values are
+    brought back to 1 at most; they would grow to infinity.)"""
+    w = ob.Mx4Linear(torch.randn(64, 64, device=DEV) * 0.2)
+    x = torch.randn(130, 64, device=DEV)
+    y, z = x.clone(), x
+    for i in range(200):
+        y = ob.onebit_mx4_dequantize(ob.onebit_mx4_quantize(w.forward(y) + x, forms="rows"))
+        y = y / y.abs().amax()
+    for i in range(200):
+        torch.cuda.synchronize()
+        z = w.forward(z)
+        torch.cuda.synchronize()
+        q = ob.onebit_mx4_quantize(z + x)
+        torch.cuda.synchronize()
+        z = ob.onebit_mx4_dequantize(q)
+        z = z / z.abs().amax()
+    assert torch.equal(y, z) and z.isfinite().all()
+
+
 def test_refusals_on_the_gpu():
     x = torch.zeros(4, 64, device=DEV)
     q = ob.onebit_mx4_quantize(x)
