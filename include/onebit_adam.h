@@ -690,7 +690,8 @@ int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* 
  *           2^(s-127); 255 makes the whole block NaN. Tiles of 128 rows by 4 blocks, 512 bytes each,
  *           all tiles of 128 rows one after another: row r, block b at
  *           ((r/128) * ceil(cols/128) + b/4) * 512 + (r%32) * 16 + (r%128/32) * 4 + b%4.
- *           Places of no block hold 0.
+ *           Places of no block hold 0. (128 rows at least: a long vector is better quantised as a
+ *           matrix of 128 rows or more than as one row.)
  * both 16-byte aligned, of the lengths that onebit_mx4_layout gives.
  *
  * Quantising a block: a = its largest magnitude; 2^k the smallest power of two, k >= -127, with
@@ -708,8 +709,10 @@ int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* 
  * themselves (eight of them, and ld a multiple of eight, are faster).
  *
  * Refused (ONEBIT_ERR_ARG, ONEBIT_ERR_ALIGN; the reason in onebit_last_error): what the above
- * excludes, and buffers that are written and overlap another of the call. Empty matrices are
- * valid; their pointers are ignored.
+ * excludes, and buffers that are written and overlap another of the call (a plain matrix from its
+ * first element to its last, what lies between its rows included). Empty matrices are valid; their
+ * pointers are ignored. The kernels may become resident before the work ahead of them in the stream
+ * has ended, and wait for all of it before they touch memory.
  * ------------------------------------------------------------------------------------------
  */
 

@@ -161,7 +161,11 @@ def tolerance(a, b, k):
 PRODUCTS = [(2, 33, 31), (3, 129, 8193), (4, 6000, 1000), (4, 40, 20000), (4, 9000, 1500), (1, 1, 1), (1, 128, 64), (1, 129, 65), (16, 127, 256), (17, 1, 257), (32, 256, 128),
             (33, 100, 31), (64, 130, 1000), (65, 128, 2048), (100, 1000, 96), (128, 128, 512),
             (129, 300, 320), (256, 256, 256), (257, 129, 513), (300, 2000, 160), (1000, 77, 999),
-            (1, 6400, 1600), (24, 5003, 1600), (2100, 2050, 700), (513, 50, 9000), (40, 40, 20000)]
+            (1, 6400, 1600), (24, 5003, 1600), (2100, 2050, 700), (513, 50, 9000), (40, 40, 20000),
+            # every width of tiles, split and not, with pairs whose second block has no columns, at
+            # strides that TMA takes and others
+            (12, 300, 5000), (9, 5003, 2100), (1000, 777, 1999), (1025, 1100, 9000), (5000, 3900, 600),
+            (3000, 3900, 2000), (4100, 1001, 4000)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
