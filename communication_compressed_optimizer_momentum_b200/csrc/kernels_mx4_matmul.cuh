@@ -56,6 +56,11 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
+// The same for a warp that runs together: all of its lanes wait, and all give up if one does.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(kFull, mm_wait(bar, parity));
+}
+
 template <int TM, bool PAIR, bool SPLIT>
 struct MmTile {
     static constexpr int kGroup = PAIR ? 2 : 1;
@@ -471,7 +476,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             place(t, tm, tn);
             const int arow = tm * TM / kAtomRows, brow = tn * S::kGroup + bank;
             for (int k = k0; k < k1; ++k) {
-                if (!(ok = mm_wait(empty + stage, phase ^ 1))) break;
+                if (!(ok = warp_wait(empty + stage, phase ^ 1))) break;
                 uint8_t* s = sm + stage * S::kStage;
                 if (elect()) {
                     mbar_arrive_expect_tx(full + stage, S::kStage);
@@ -503,11 +508,11 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const uint32_t d = tmem + (uint32_t)(i & 1) * S::kSecond;
             const int before = S::kOverlap > 0 ? i - 1 : i - 2;  // the tile that has to be read first
             if (before >= 0 &&
-                !(ok = mm_wait(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
+                !(ok = warp_wait(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
                 break;
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = mm_wait(ready + stage, phase))) break;
+                if (!(ok = warp_wait(ready + stage, phase))) break;
                 tc_fence_after();
                 const uint32_t s = smem_addr(sm + stage * S::kStage);
                 const uint32_t eb = tmem + S::kExp + (c % S::kExpBuffers) * S::kExpCols, ea = eb + 8;
@@ -530,7 +535,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             if (ok && elect()) tc_commit<PAIR>(done + (i & 1));
             __syncwarp();
         }
-        if (!ok && lane == 0) {
+        if (!ok && elect()) {  // (the lane that issued them)
             atomicOr(&g_mx4_status, kMmTimeout);
             tc_commit<PAIR>(last);
             mm_wait(last, 0);
@@ -548,7 +553,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const int rows = (int)min((int64_t)TM, p.m - m0);
             w.n0 = (tn * S::kGroup + bank) * kMmLanes + quad * 32;
             constexpr int kC = S::kChunk;
-            if (!(ok = mm_wait(done + buf, (uint32_t)(i >> 1) & 1))) break;
+            if (!(ok = warp_wait(done + buf, (uint32_t)(i >> 1) & 1))) break;
             tc_fence_after();
             const auto read_done = [&] {
                 tc_fence_before();
@@ -624,7 +629,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             // since the tensor cores take exponents from even columns on only
             const int sub = TM < kAtomRows ? tm * TM % kAtomRows / 32 : 0;
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = mm_wait(full + stage, phase))) break;
+                if (!(ok = warp_wait(full + stage, phase))) break;
                 const uint4* e = reinterpret_cast<const uint4*>(sm + stage * S::kStage + S::kB + S::kA) +
                                  lane;
                 const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kExp +
@@ -644,7 +649,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                 // the stage itself, for which its loads have waited)
                 const int b = c - S::kExpBuffers;
                 if (S::kExpBuffers < S::kStages && b >= 0 &&
-                    !(ok = mm_wait(empty + b % S::kStages, (uint32_t)(b / S::kStages) & 1)))
+                    !(ok = warp_wait(empty + b % S::kStages, (uint32_t)(b / S::kStages) & 1)))
                     break;
                 __syncwarp();
                 tc_fence_after();

@@ -60,6 +60,27 @@ int64_t mx4_span(int64_t rows, int64_t cols, int64_t ld, int64_t w) {
     return rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * w;
 }
 
+// The address ranges of one call, few enough to be compared in pairs (Ranges, for lists, allocates):
+// what is written must not overlap anything else.
+struct Spans {
+    static constexpr int kMost = 8;
+    uintptr_t lo[kMost], hi[kMost];
+    bool write[kMost];
+    int n = 0;
+    void add(const void* p, int64_t bytes, bool w) {
+        if (p == nullptr || bytes <= 0) return;
+        lo[n] = reinterpret_cast<uintptr_t>(p);
+        hi[n] = lo[n] + (uintptr_t)bytes;
+        write[n++] = w;
+    }
+    bool clash() const {
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < i; ++j)
+                if ((write[i] || write[j]) && lo[i] < hi[j] && lo[j] < hi[i]) return true;
+        return false;
+    }
+};
+
 // Shared memory beyond 48 KB is asked for once for each kernel and device.
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -402,18 +423,18 @@ int onebit_mx4_quantize(int64_t rows, int64_t cols, const void* x, int32_t dtype
         if (rc == ONEBIT_OK && residual != nullptr)
             rc = mx4_plain(where, "residual", rows, cols, residual, ld_residual, 4);
         if (rc != ONEBIT_OK) return rc;
-        Ranges ranges;
-        ranges.add(0, x, mx4_span(rows, cols, ld, width(dtype)), false);
+        Spans spans;
+        spans.add(x, mx4_span(rows, cols, ld, width(dtype)), false);
         if (codes != nullptr) {
-            ranges.add(1, codes, mx4_code_bytes(rows, cols), true);
-            ranges.add(1, scales, mx4_scale_bytes(rows, cols), true);
+            spans.add(codes, mx4_code_bytes(rows, cols), true);
+            spans.add(scales, mx4_scale_bytes(rows, cols), true);
         }
         if (codes_t != nullptr) {
-            ranges.add(2, codes_t, mx4_code_bytes(cols, rows), true);
-            ranges.add(2, scales_t, mx4_scale_bytes(cols, rows), true);
+            spans.add(codes_t, mx4_code_bytes(cols, rows), true);
+            spans.add(scales_t, mx4_scale_bytes(cols, rows), true);
         }
-        if (residual != nullptr) ranges.add(3, residual, mx4_span(rows, cols, ld_residual, 4), true);
-        if (ranges.clash()) return bad(where, "what is written overlaps something else");
+        if (residual != nullptr) spans.add(residual, mx4_span(rows, cols, ld_residual, 4), true);
+        if (spans.clash()) return bad(where, "what is written overlaps something else");
         return mx4_quantize(rows, cols, x, dtype, ld, codes, scales, codes_t, scales_t,
                             stochastic, seed, residual, ld_residual, as_stream(stream));
     });
@@ -431,11 +452,11 @@ int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, cons
         if (rc != ONEBIT_OK || rows == 0 || cols == 0) return rc;
         rc = mx4_tiles(where, rows, cols);
         if (rc != ONEBIT_OK) return rc;
-        Ranges ranges;
-        ranges.add(0, codes, mx4_code_bytes(rows, cols), false);
-        ranges.add(1, scales, mx4_scale_bytes(rows, cols), false);
-        ranges.add(2, out, mx4_span(rows, cols, ld, width(dtype)), true);
-        if (ranges.clash()) return bad(where, "out overlaps the codes or exponents");
+        Spans spans;
+        spans.add(codes, mx4_code_bytes(rows, cols), false);
+        spans.add(scales, mx4_scale_bytes(rows, cols), false);
+        spans.add(out, mx4_span(rows, cols, ld, width(dtype)), true);
+        if (spans.clash()) return bad(where, "out overlaps the codes or exponents");
         Mx4DequantArgs a{};
         a.c = codes;
         a.s = scales;
@@ -474,15 +495,15 @@ int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
         if (rc == ONEBIT_OK) rc = mx4_plain(where, "out", m, n, out, ld, width(dtype));
         if (rc == ONEBIT_OK) rc = mx4_out_size(where, m, n);
         if (rc != ONEBIT_OK) return rc;
-        Ranges ranges;
+        Spans spans;
         if (k > 0) {
-            ranges.add(0, a_codes, mx4_code_bytes(m, k), false);
-            ranges.add(0, a_scales, mx4_scale_bytes(m, k), false);
-            ranges.add(1, b_codes, mx4_code_bytes(n, k), false);
-            ranges.add(1, b_scales, mx4_scale_bytes(n, k), false);
+            spans.add(a_codes, mx4_code_bytes(m, k), false);
+            spans.add(a_scales, mx4_scale_bytes(m, k), false);
+            spans.add(b_codes, mx4_code_bytes(n, k), false);
+            spans.add(b_scales, mx4_scale_bytes(n, k), false);
         }
-        ranges.add(2, out, mx4_span(m, n, ld, width(dtype)), true);
-        if (ranges.clash()) return bad(where, "out overlaps an operand");
+        spans.add(out, mx4_span(m, n, ld, width(dtype)), true);
+        if (spans.clash()) return bad(where, "out overlaps an operand");
         const cudaStream_t st = as_stream(stream);
         if (k == 0) return accumulate ? ONEBIT_OK : mx4_clear(out, m, n, ld, width(dtype), st);
         return mx4_product(m, n, k, a_codes, a_scales, b_codes, b_scales, out, dtype, ld, accumulate,
@@ -510,24 +531,24 @@ int onebit_mx4_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_
         if (rc == ONEBIT_OK) rc = mx4_out_size(where, m, n);
         if (rc == ONEBIT_OK) rc = mx4_tiles(where, m, k);
         if (rc != ONEBIT_OK || m == 0) return rc;
-        Ranges ranges;
+        Spans spans;
         if (k > 0) {
-            ranges.add(0, x, mx4_span(m, k, ld_x, width(x_dtype)), false);
+            spans.add(x, mx4_span(m, k, ld_x, width(x_dtype)), false);
             if (n > 0) {
-                ranges.add(1, b_codes, mx4_code_bytes(n, k), false);
-                ranges.add(1, b_scales, mx4_scale_bytes(n, k), false);
+                spans.add(b_codes, mx4_code_bytes(n, k), false);
+                spans.add(b_scales, mx4_scale_bytes(n, k), false);
             }
             if (!few) {
-                ranges.add(2, a_codes, mx4_code_bytes(m, k), true);
-                ranges.add(2, a_scales, mx4_scale_bytes(m, k), true);
+                spans.add(a_codes, mx4_code_bytes(m, k), true);
+                spans.add(a_scales, mx4_scale_bytes(m, k), true);
             }
             if (kept) {
-                ranges.add(2, a_codes_t, mx4_code_bytes(k, m), true);
-                ranges.add(2, a_scales_t, mx4_scale_bytes(k, m), true);
+                spans.add(a_codes_t, mx4_code_bytes(k, m), true);
+                spans.add(a_scales_t, mx4_scale_bytes(k, m), true);
             }
         }
-        ranges.add(3, out, mx4_span(m, n, ld, width(dtype)), true);
-        if (ranges.clash()) return bad(where, "what is written overlaps something else");
+        spans.add(out, mx4_span(m, n, ld, width(dtype)), true);
+        if (spans.clash()) return bad(where, "what is written overlaps something else");
         const cudaStream_t st = as_stream(stream);
         if (k == 0) return n > 0 ? mx4_clear(out, m, n, ld, width(dtype), st) : ONEBIT_OK;
         if (few) {

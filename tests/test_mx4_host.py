@@ -253,3 +253,17 @@ def test_linear_binding_refuses_what_is_not_on_the_gpu():
         ob.onebit_mx4_linear(torch.zeros(2, 64), w)
     with pytest.raises(TypeError, match="Mx4"):
         ob.onebit_mx4_linear(torch.zeros(2, 64), torch.zeros(40, 64))
+
+
+def test_everything_raises_without_the_library(monkeypatch):
+    w = ob.Mx4.empty(4, 32, device="cpu")
+    monkeypatch.setattr(_abi, "LIB_PATH", "/nonexistent/libonebit_adam.so")
+    monkeypatch.setattr(_abi, "_lib", None)
+    monkeypatch.setattr(ob.adamw, "_native", None)
+    x = torch.zeros(4, 32)
+    for call in (lambda: ob.onebit_mx4_layout(1, 1), lambda: ob.onebit_mx4_linear_needs(1, 1, 1),
+                 lambda: ob.onebit_mx4_quantize(x), lambda: ob.onebit_mx4_dequantize(w),
+                 lambda: ob.onebit_mx4_matmul(w, w), lambda: ob.onebit_mx4_linear(x, w),
+                 lambda: ob.onebit_mx4_status(0), lambda: ob.Mx4Linear(x)):
+        with pytest.raises(RuntimeError, match="not built"):
+            call()
