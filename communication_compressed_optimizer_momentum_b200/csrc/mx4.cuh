@@ -255,37 +255,48 @@ int launch_mx4_matmul(MmOperands o, int split, cudaStream_t st) {
     return launch_mx4(kernel, grid, kMmThreads, S::kSmem, PAIR ? 2 : split, st, maps, o.args);
 }
 
-template <typename OT>
-int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
-    const int64_t tn = ceil_div(o.n, kMmLanes), stages = o.args.stages;
+// The tiles of a product: rows of out, and the blocks that share one tile's common axis (1: none do).
+struct MmChoice {
+    int rows, split;
+};
+MmChoice choose_tiles(int64_t m, int64_t n, int64_t stages, bool wide) {
+    const int64_t tn = ceil_div(n, kMmLanes);
     // Few rows: narrow tiles; what they leave idle takes parts of the common axis, of four stages and
     // more (16 x 4096 from 4096: 6.7 us in four parts, 7.2 in one; from 1024: 7.1 and 4.5).
-    const auto spare = [&](int tm) {
-        return (int)std::min<int64_t>(std::min<int64_t>(8, kSms / (tn * ceil_div(o.m, tm))), stages / 4);
+    const auto narrow = [&](int tm) {
+        const int64_t split =
+            std::min<int64_t>(std::min<int64_t>(8, kSms / (tn * ceil_div(m, tm))), stages / 4);
+        return MmChoice{tm, (int)std::max<int64_t>(split, 1)};
     };
-    if (o.m <= 16) {
-        const int split = spare(16);
-        if (split > 1) return launch_mx4_matmul<16, false, OT, true>(o, split, st);
-        return launch_mx4_matmul<16, false, OT, false>(o, 1, st);
-    }
+    if (m <= 16) return narrow(16);
     // What a launch takes, in 10 ns, as measured: once, and a round of tiles by its stages and by what
     // it writes. (4096 x 4096 from 1024: tiles of 64 rows 14.0 us, 128 10.2, 256 10.1; 1024 x 1024 from
     // 1024: 5.0, 5.5, 7.3; 512 x 4096 from 4096: 13.4, 8.9, 11.2.)
-    const bool wide = sizeof(OT) == 4;
     const auto cost = [&](int tm, int group, int64_t once, int64_t stage, int64_t tile) {
-        const int64_t tiles = ceil_div(o.m, tm) * ceil_div(o.n, kMmLanes * group);
+        const int64_t tiles = ceil_div(m, tm) * ceil_div(n, kMmLanes * group);
         return once + ceil_div(tiles, kSms / group) * (stages * stage + tile);
     };
     const int64_t c32 = cost(32, 1, 390, 20, 30), c64 = cost(64, 1, 390, 22, wide ? 60 : 40),
                   c128 = cost(128, 1, 400, 24, wide ? 120 : 60),
                   c256 = cost(256, 2, 590, 31, wide ? 250 : 80);
     const int64_t best = std::min(std::min(c32, c64), std::min(c128, c256));
-    if (best == c256) return launch_mx4_matmul<256, true, OT, false>(o, 1, st);
-    if (best == c128) return launch_mx4_matmul<128, false, OT, false>(o, 1, st);
-    if (best == c64) return launch_mx4_matmul<64, false, OT, false>(o, 1, st);
-    const int split = spare(32);
-    if (split > 1) return launch_mx4_matmul<32, false, OT, true>(o, split, st);
-    return launch_mx4_matmul<32, false, OT, false>(o, 1, st);
+    if (best == c256) return {256, 1};
+    if (best == c128) return {128, 1};
+    if (best == c64) return {64, 1};
+    return narrow(32);
+}
+
+template <typename OT>
+int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
+    const MmChoice t = choose_tiles(o.m, o.n, o.args.stages, sizeof(OT) == 4);
+    if (t.rows == 256) return launch_mx4_matmul<256, true, OT, false>(o, 1, st);
+    if (t.rows == 128) return launch_mx4_matmul<128, false, OT, false>(o, 1, st);
+    if (t.rows == 64) return launch_mx4_matmul<64, false, OT, false>(o, 1, st);
+    if (t.rows == 32)
+        return t.split > 1 ? launch_mx4_matmul<32, false, OT, true>(o, t.split, st)
+                           : launch_mx4_matmul<32, false, OT, false>(o, 1, st);
+    return t.split > 1 ? launch_mx4_matmul<16, false, OT, true>(o, t.split, st)
+                       : launch_mx4_matmul<16, false, OT, false>(o, 1, st);
 }
 
 // At most kFewRows rows of x, which is in 4 bits (XT uint8_t) or plain.
@@ -577,6 +588,17 @@ int onebit_mx4_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_
 }
 
 int onebit_mx4_linear_needs(int64_t m, int64_t n, int64_t k) { return mx4_few(m, n, k, true) ? 0 : 1; }
+
+// For tests, not part of the C ABI: what a product of these sizes (none 0) is made with. rows: of a tile
+// of out, 0 without the tensor cores; split: blocks that share a tile's common axis. Host only.
+void onebit_internal_mx4_tiles(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t* rows,
+                               int32_t* split) {
+    const MmChoice t = mx4_few(m, n, k, false)
+                           ? MmChoice{0, 1}
+                           : choose_tiles(m, n, ceil_div(k, kStageCols), dtype == ONEBIT_F32);
+    *rows = t.rows;
+    *split = t.split;
+}
 
 int onebit_mx4_status(uint32_t* flags, void* stream) {
     return guarded([&]() -> int {
