@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kMxThreads, 2) k_mx4_few(const Mx4FewArgs p) {
     after_what_is_ahead();
     // a block's two halves change places in every other four blocks: eight lanes read different banks
     __shared__ uint4 xv[MT][2 * kFewBlocks];
-    __shared__ float xf[MT][kFewBlocks];                // a quarter of the block's power of two
+    __shared__ float xf[MT][kFewBlocks];                // an eighth of the block's power of two
     __shared__ int xs[MT][kFewBlocks];                  // what the bias of b's bytes adds, negative
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (p.k + kMxBlk - 1) / kMxBlk;
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kMxThreads, 2) k_mx4_few(const Mx4FewArgs p) {
             xv[t][2 * l + swap] = make_uint4(v[0], v[1], v[2], v[3]);
             xv[t][2 * l + (swap ^ 1)] = make_uint4(v[4], v[5], v[6], v[7]);
             xs[t][l] = sum;
-            xf[t][l] = 0.25f * mx4_scale(k);
+            xf[t][l] = 0.125f * mx4_scale(k);
         }
     };
     // This lane's block b of rows r, r + 32, r + 64, r + 96 of the atom.
@@ -851,12 +851,13 @@ __global__ void __launch_bounds__(kMxThreads, 2) k_mx4_few(const Mx4FewArgs p) {
                     int s = bias;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) s = __dp4a((int)x[i], (int)v[g][i], s);
-                    // the sum (at most 4608) as a float, by way of 1.5 * 2^23; a scale that overflows
-                    // must not make NaN of a sum of 0, a NaN one must
-                    const float whole = __fsub_rn(__int_as_float(s + 0x4b400000), 12582912.0f);
+                    // twice the sum (at most 4608) as a float, by way of 1.5 * 2^24. A scale that
+                    // overflows must not make NaN of a sum of 0, a NaN one must; with the largest
+                    // number in its place 2 and more still overflow (1 would not).
+                    const float twice = __fsub_rn(__int_as_float(s + 0x4bc00000), 25165824.0f);
                     float scale = __fmul_rn(f, scales[g]);
                     asm("min.NaN.f32 %0, %1, %2;" : "=f"(scale) : "f"(scale), "f"(3.402823466e38f));
-                    acc[g][t] = __fmaf_rn(whole, scale, acc[g][t]);
+                    acc[g][t] = __fmaf_rn(twice, scale, acc[g][t]);
                 }
             }
         }

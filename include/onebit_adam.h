@@ -739,8 +739,8 @@ int onebit_mx4_dequantize(int64_t rows, int64_t cols, const uint8_t* codes, cons
 /*
  * out = a b^T, or out + a b^T with accumulate = 1 (fp32 only): a is m x k, b is n x k, both in 4
  * bits; out [m][ld] fp32 or bf16 by dtype. Sums in fp32 on the tensor cores, in an order that the
- * sizes alone fix; products below fp32's range are lost, and an accumulated value may become 0 if it is
- * below 2^-126. A NaN block makes its row of a (its column
+ * sizes alone fix; what is beyond fp32's range is infinite, and parts of a sum below 2^-126 (and with
+ * accumulate = 1 out's own values below it) may count as 0. A NaN block makes its row of a (its column
  * of out, for b) NaN. k = 0 gives zeros (accumulate: out as it was).
  */
 int onebit_mx4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,

@@ -69,3 +69,25 @@ def test_exact_products_of_every_tile(m, n, k, wide, narrow):
     assert torch.equal(ob.onebit_mx4_matmul(qa, qb, out=base.clone(), accumulate=True),
                        (base + want).float())
     assert ob.onebit_mx4_status() == 0
+
+
+@pytest.mark.parametrize("m", [1, 2, 4, 5, 40])
+def test_sums_beyond_the_range_of_fp32(m):
+    """Blocks whose products cancel but for one, +-1/4 times a power of two: the result is that value as
+    fp32 holds it, infinity from 2^128 on, and 0 where all of them cancel, with and without tensor cores
+    and for plain values."""
+    x = torch.zeros(m, 70, device=DEV)
+    w = torch.zeros(40, 70, device=DEV)
+    for i, at in enumerate((0, 32)):
+        x[:, at:at + 3] = torch.tensor([6, 6, 0.5], device=DEV)
+        for r, last in enumerate((0.5, -0.5, 0.0)):
+            w[r, at:at + 3] = torch.tensor([6, -6, last if i == 0 else 0], device=DEV)
+    for ex, ew in ((120, 12), (120, 10), (120, 9), (10, 119), (124, 124), (-126, 124), (60, 70), (0, 0)):
+        qx, qw = ob.onebit_mx4_quantize(x * 2.0 ** ex), ob.onebit_mx4_quantize(w * 2.0 ** ew)
+        a, b = (ob.onebit_mx4_dequantize(q).double() for q in (qx, qw))
+        want = (a @ b.t()).float()
+        assert float(want[0, 0]) == (2.0 ** (ex + ew - 2) if ex + ew < 130 else float("inf"))
+        assert torch.equal(want[:, 1], -want[:, 0]) and (want[:, 2:] == 0).all()
+        assert torch.equal(ob.onebit_mx4_matmul(qx, qw, dtype=F32), want)
+        assert torch.equal(ob.onebit_mx4_linear(x * 2.0 ** ex, qw), want)
+        assert torch.equal(ob.onebit_mx4_matmul(qx, qw), want.bfloat16())
