@@ -185,6 +185,15 @@ class Mx4Linear:
             raise ValueError("weight must be a matrix of %d x %d" % (self.outer, self.inner))
         if weight.device != self.device:
             raise ValueError("weight is on %s, expected %s" % (weight.device, self.device))
+        if weight.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("weight must be float32 or bfloat16, got %s" % weight.dtype)
+        if weight.is_contiguous():
+            return
+        rows, cols = weight.stride()
+        if self.inner > 1 and cols != 1:
+            raise ValueError("weight must have consecutive columns")
+        if self.outer > 1 and self.inner > 0 and rows < self.inner:
+            raise ValueError("weight must have rows of its own: they are %d apart" % rows)
 
     def update(self, weight, stream=None) -> None:
         """Quantise the weights anew."""
