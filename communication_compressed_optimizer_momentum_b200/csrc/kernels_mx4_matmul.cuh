@@ -35,15 +35,16 @@ constexpr int kOutWarps = 8;              // write out
 constexpr int kMmLanes = 128;             // rows of b in a block's part of a tile
 constexpr int kStageCols = 256;
 constexpr uint32_t kMmTimeout = 1u;
-constexpr uint64_t kMmWaitNs = 20ull * 1000 * 1000 * 1000;   // of one wait; the longest tile takes one
+constexpr uint64_t kMmWaitNs = 20ull * 1000 * 1000 * 1000;   // the longest tile takes a second
 constexpr int kOutBytes = 2048;           // written out at a time: 32 columns of out by 32 rows (bf16)
 constexpr int kOutRows32 = 16;            // ... or by 16 (fp32)
 
 __device__ uint32_t g_mx4_status;
 
-// Wait for phase `parity` of the barrier, giving up after kMmWaitNs (a long common axis keeps the warps
-// that write out waiting for a good while: a number of polls would not say how long).
-__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity) {
+// Wait for phase `parity` of the barrier, giving up after `limit` ns (a long common axis keeps the warps
+// that write out waiting for a good while: a number of polls would not say how long; 256 polls take 1 ms
+// where nothing comes).
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
     for (int i = 0; i < 256; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     uint64_t start, now;
@@ -52,13 +53,13 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity) {
         for (int i = 0; i < 256; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-    } while (now - start < kMmWaitNs);
+    } while (now - start < limit);
     return false;
 }
 
 // The same for a warp that runs together: all of its lanes wait, and all give up if one does.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(kFull, mm_wait(bar, parity));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    return __all_sync(kFull, mm_wait(bar, parity, limit));
 }
 
 template <int TM, bool PAIR, bool SPLIT>
@@ -105,6 +106,7 @@ struct Mx4MatmulArgs {
     int32_t tiles_m, tiles_n;
     int32_t accumulate;
     int32_t tma;               // out's address and rows are aligned to 16 bytes
+    uint64_t wait_ns;          // after which a wait gives up
 };
 
 __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y,
@@ -465,6 +467,9 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
         tm = r / wide;
         tn = band * kBand + r % wide;
     };
+    // A warp that gives up stops, and those that depend on it do likewise, each for itself: what is
+    // in flight is waited for at the end by the warp that has started it, whether it has given up or
+    // not, and with a limit of its own, since copies and products that have been issued do end.
     bool ok = true;
 
     if (warp == 0) {
@@ -476,7 +481,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             place(t, tm, tn);
             const int arow = tm * TM / kAtomRows, brow = tn * S::kGroup + bank;
             for (int k = k0; k < k1; ++k) {
-                if (!(ok = warp_wait(empty + stage, phase ^ 1))) break;
+                if (!(ok = warp_wait(empty + stage, phase ^ 1, p.wait_ns))) break;
                 uint8_t* s = sm + stage * S::kStage;
                 if (elect()) {
                     mbar_arrive_expect_tx(full + stage, S::kStage);
@@ -493,11 +498,14 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                 }
             }
         }
-        if (!ok && lane == 0) {  // leave no copy in flight behind
-            atomicOr(&g_mx4_status, kMmTimeout);
+        if (lane == 0) {         // leave no copy in flight behind
             for (int64_t f = filled > S::kStages ? filled - S::kStages : 0; f < filled; ++f)
-                mm_wait(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1);
+                ok = mm_wait(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1, kMmWaitNs) && ok;
+            // ... nor an arrival from a pair's other block, which may wait as long for one thing more
+            if (PAIR && bank == 1) ok = mm_wait(last, 0, 4 * kMmWaitNs) && ok;
+            if (!ok) atomicOr(&g_mx4_status, kMmTimeout);
         }
+        __syncwarp();
     } else if (warp == 1 && bank == 0) {
         int stage = 0, c = 0;
         uint32_t phase = 0;
@@ -508,11 +516,11 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const uint32_t d = tmem + (uint32_t)(i & 1) * S::kSecond;
             const int before = S::kOverlap > 0 ? i - 1 : i - 2;  // the tile that has to be read first
             if (before >= 0 &&
-                !(ok = warp_wait(drained + (before & 1), (uint32_t)(before >> 1) & 1)))
+                !(ok = warp_wait(drained + (before & 1), (uint32_t)(before >> 1) & 1, p.wait_ns)))
                 break;
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = warp_wait(ready + stage, phase))) break;
+                if (!(ok = warp_wait(ready + stage, phase, p.wait_ns))) break;
                 tc_fence_after();
                 const uint32_t s = smem_addr(sm + stage * S::kStage);
                 const uint32_t eb = tmem + S::kExp + (c % S::kExpBuffers) * S::kExpCols, ea = eb + 8;
@@ -535,10 +543,10 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             if (ok && elect()) tc_commit<PAIR>(done + (i & 1));
             __syncwarp();
         }
-        if (!ok && elect()) {  // (the lane that issued them)
-            atomicOr(&g_mx4_status, kMmTimeout);
+        if (elect()) {           // (the lane that issued them)
             tc_commit<PAIR>(last);
-            mm_wait(last, 0);
+            ok = mm_wait(last, 0, kMmWaitNs) && ok;
+            if (!ok) atomicOr(&g_mx4_status, kMmTimeout);
         }
     } else if (warp >= 2 && warp < 2 + kOutWarps) {
         const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -553,7 +561,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const int rows = (int)min((int64_t)TM, p.m - m0);
             w.n0 = (tn * S::kGroup + bank) * kMmLanes + quad * 32;
             constexpr int kC = S::kChunk;
-            if (!(ok = warp_wait(done + buf, (uint32_t)(i >> 1) & 1))) break;
+            if (!(ok = warp_wait(done + buf, (uint32_t)(i >> 1) & 1, p.wait_ns))) break;
             tc_fence_after();
             const auto read_done = [&] {
                 tc_fence_before();
@@ -629,7 +637,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             // since the tensor cores take exponents from even columns on only
             const int sub = TM < kAtomRows ? tm * TM % kAtomRows / 32 : 0;
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = warp_wait(full + stage, phase))) break;
+                if (!(ok = warp_wait(full + stage, phase, p.wait_ns))) break;
                 const uint4* e = reinterpret_cast<const uint4*>(sm + stage * S::kStage + S::kB + S::kA) +
                                  lane;
                 const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S::kExp +
@@ -649,7 +657,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                 // the stage itself, for which its loads have waited)
                 const int b = c - S::kExpBuffers;
                 if (S::kExpBuffers < S::kStages && b >= 0 &&
-                    !(ok = warp_wait(empty + b % S::kStages, (uint32_t)(b / S::kStages) & 1)))
+                    !(ok = warp_wait(empty + b % S::kStages, (uint32_t)(b / S::kStages) & 1, p.wait_ns)))
                     break;
                 __syncwarp();
                 tc_fence_after();

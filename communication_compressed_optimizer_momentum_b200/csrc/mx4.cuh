@@ -299,6 +299,9 @@ int queue_mx4_matmul(const MmOperands& o, cudaStream_t st) {
                        : launch_mx4_matmul<16, false, OT, false>(o, 1, st);
 }
 
+// The limit of a product's waits (onebit_internal_mx4_wait).
+std::atomic<uint64_t> g_mx4_wait_ns{kMmWaitNs};
+
 // At most kFewRows rows of x, which is in 4 bits (XT uint8_t) or plain.
 template <typename XT, typename OT>
 int queue_mx4_few(const Mx4FewArgs& a, cudaStream_t st) {
@@ -352,6 +355,7 @@ int mx4_product(int64_t m, int64_t n, int64_t k, const void* a, const void* sa, 
     o.args.steps = (int32_t)ceil_div(k, 64);
     o.args.stages = (int32_t)ceil_div(k, kStageCols);
     o.args.accumulate = accumulate;
+    o.args.wait_ns = g_mx4_wait_ns.load(std::memory_order_relaxed);
     o.args.tma = aligned16(out) && (m == 1 || (ld * width(dtype) % 16 == 0 &&
                                                ld * width(dtype) < (int64_t)1 << 40));
     return dtype == ONEBIT_F32 ? queue_mx4_matmul<float>(o, st)
@@ -599,6 +603,10 @@ void onebit_internal_mx4_tiles(int64_t m, int64_t n, int64_t k, int32_t dtype, i
     *rows = t.rows;
     *split = t.split;
 }
+
+// For tests, not part of the C ABI: after how many ns the waits of products that are queued from now on
+// give up; 0: the 20 s that they have otherwise. Host only.
+void onebit_internal_mx4_wait(uint64_t ns) { g_mx4_wait_ns.store(ns != 0 ? ns : kMmWaitNs); }
 
 int onebit_mx4_status(uint32_t* flags, void* stream) {
     return guarded([&]() -> int {
