@@ -41,25 +41,44 @@ constexpr int kOutRows32 = 16;            // ... or by 16 (fp32)
 
 __device__ uint32_t g_mx4_status;
 
+// Whether phase `parity` of the barrier is over, seen without ordering memory, for arrivals from all of a
+// cluster.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Wait for phase `parity` of the barrier, giving up after `limit` ns (a long common axis keeps the warps
 // that write out waiting for a good while: a number of polls would not say how long; 256 polls take 1 ms
 // where nothing comes).
+// PAIR: arrivals come from the other block too (pair_arrive).
+template <bool PAIR = false>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    const auto there = [&] {
+        return PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+    };
     for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+        if (there()) return true;
     uint64_t start, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
     do {
         for (int i = 0; i < 256; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (there()) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
     } while (now - start < limit);
     return false;
 }
 
 // The same for a warp that runs together: all of its lanes wait, and all give up if one does.
+template <bool PAIR = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
-    return __all_sync(kFull, mm_wait(bar, parity, limit));
+    return __all_sync(kFull, mm_wait<PAIR>(bar, parity, limit));
 }
 
 template <int TM, bool PAIR, bool SPLIT>
@@ -252,14 +271,23 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Arrive on a barrier of a pair's first block. What the arrival announces are finished copies (TMA) and
-// stores to tensor memory, which the tensor cores of the arriving block's own SM read, and no plain
-// stores: the arrival needs no fence of the cluster's scope (with one, 8192^3 takes 423 us, without
-// 240).
+// Arrive on a barrier of a pair's first block, which issues the products of both. Relaxed, at the
+// cluster's scope: no memory is ordered by the arrival and by the wait for it themselves (with a release
+// at this scope a warp stands still for 1000 clocks: 8192^3 takes 423 us, without 240; one warp that
+// passes the others' arrivals on with a release: 400, where 180 are reached without).
+// - Tensor memory (the exponents that are stored, the accumulators that are read) is ordered by the
+//   tensor cores' own fences: the operation and its wait, tcgen05.fence::before_thread_sync, a relaxed
+//   arrival; a relaxed wait, tcgen05.fence::after_thread_sync, the product. PTX gives this pattern.
+// - The second block's codes are copied by TMA, seen to be complete by the second block's warps (an
+//   acquire on the barrier that counts their bytes) before they arrive, and read by the tensor cores of
+//   the SM whose shared memory holds them. PTX's memory model has no rule that carries the first block's
+//   product behind this chain, which holds an arrival without release: it rests on shared memory being
+//   in one place. A copy counts its bytes where it has written them, nothing keeps other copies of them,
+//   and the product is issued after the arrival. (Products repeat bit for bit; tests compare them in full.)
 template <bool PAIR>
 __device__ __forceinline__ void pair_arrive(uint64_t* bar) {
     if constexpr (PAIR)
-        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                          cluster_addr(smem_addr(bar), 0))
                      : "memory");
     else
@@ -516,11 +544,11 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             const uint32_t d = tmem + (uint32_t)(i & 1) * S::kSecond;
             const int before = S::kOverlap > 0 ? i - 1 : i - 2;  // the tile that has to be read first
             if (before >= 0 &&
-                !(ok = warp_wait(drained + (before & 1), (uint32_t)(before >> 1) & 1, p.wait_ns)))
+                !(ok = warp_wait<PAIR>(drained + (before & 1), (uint32_t)(before >> 1) & 1, p.wait_ns)))
                 break;
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = warp_wait(ready + stage, phase, p.wait_ns))) break;
+                if (!(ok = warp_wait<PAIR>(ready + stage, phase, p.wait_ns))) break;
                 tc_fence_after();
                 const uint32_t s = smem_addr(sm + stage * S::kStage);
                 const uint32_t eb = tmem + S::kExp + (c % S::kExpBuffers) * S::kExpCols, ea = eb + 8;
