@@ -93,7 +93,8 @@ def onebit_mx4_quantize(x, forms: str = "rows", rounding: str = "nearest", seed:
 
     forms: "rows" gives the matrix, in blocks of 32 of a row; "columns" its transpose, in blocks of
     32 of a column; "both" the pair (matrix, transpose) from one pass over x. rounding: "nearest", or
-    "stochastic" with the random bits of seed (and seed + 1 for the transpose). residual (a float32
+    "stochastic" with the random bits of seed (and seed + 1 for the transpose: seeds of calls whose errors
+    are to be unrelated are two or more apart). residual (a float32
     matrix of x's size, with forms="rows"): error feedback; x + residual is quantised, and residual
     becomes what that lost. out: an ``Mx4`` (with "both" a pair) to write to, else new ones."""
     rows, columns = _one_of(_FORMS, forms, "forms")
@@ -213,7 +214,9 @@ class Mx4Linear:
         """(dx, dW) for dy [..., outer]. dx is of ``dtype`` (dy's by default), None without need_dx.
         dW comes from what ``forward`` kept (without it None): a float32 matrix, or into grad (float32
         or bfloat16), added to it with accumulate (float32). seed selects the random bits that dy is
-        rounded with: another one for every call."""
+        rounded with, those of seed for dx and of seed + 1 for dW: every call of every layer and step takes
+        one of its own, two or more from all others (2 * (step * layers + layer), say). With the same or
+        the next number every value still keeps its mean, but calls share their errors place by place."""
         if kept is None and (grad is not None or accumulate):
             raise ValueError("grad and accumulate need what forward kept")
         if accumulate and grad is None:

@@ -721,8 +721,9 @@ int onebit_mx4_layout(int64_t rows, int64_t cols, int64_t* code_bytes, int64_t* 
 
 /*
  * Quantise x (fp32 or bf16 by dtype): codes and scales receive the matrix, codes_t and scales_t its
- * transpose (cols x rows, blocks along x's rows; its random bits are those of seed + 1). Either
- * codes or codes_t may be NULL; both are written from one pass over x.
+ * transpose (cols x rows, blocks along x's rows; its random bits are those of seed + 1, so that calls
+ * whose errors are to be unrelated take seeds that are two or more apart). Either codes or codes_t may
+ * be NULL; both are written from one pass over x.
  * residual (or NULL; fp32 [rows][ld_residual], with codes alone): error feedback. y = x + residual
  * (one fp32 addition) is quantised instead of x, and residual = y - its value (one fp32 subtraction,
  * exact when rounding to nearest; NaN in a NaN block).

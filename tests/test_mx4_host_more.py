@@ -1,8 +1,10 @@
-"""Mx4Linear's checks of a weight, without a GPU."""
+"""Mx4Linear without a GPU: the checks of a weight, and the seeds of its backward pass."""
+import numpy as np
 import pytest
 import torch
 
 import communication_compressed_optimizer_momentum_b200 as ob
+import mx4_reference as ref
 
 
 def linear(outer, inner):
@@ -37,3 +39,15 @@ def test_weights_that_update_takes():
     linear(1, 40).check_weight(torch.zeros(40).expand(1, 40))        # one row: its stride means nothing
     linear(40, 1).check_weight(torch.zeros(40, 5)[:, 2:3])
     linear(40, 0).check_weight(torch.zeros(40, 0))
+
+
+def test_seeds_two_apart_share_no_bits():
+    """The transposed form takes the bits of seed + 1, and so does the row form of the next seed: of seeds
+    two apart, as layers and steps are to take them, no two forms have the same key."""
+    place = np.arange(4096)
+    layers, steps = 3, 4
+    seeds = [2 * (step * layers + layer) for step in range(steps) for layer in range(layers)]
+    bits = [ref.random16(place, s + form) for s in seeds for form in (0, 1)]
+    assert len({b.tobytes() for b in bits}) == 2 * len(seeds)
+    for i, a in enumerate(bits):                       # equal by chance only: 1 in 65536
+        assert all((a == b).sum() < 8 for b in bits[:i])
