@@ -89,7 +89,8 @@ def _one_of(table, value, name: str):
 
 def onebit_mx4_quantize(x, forms: str = "rows", rounding: str = "nearest", seed: int = 0,
                         residual=None, out=None, stream=None):
-    """Quantise a float32 or bfloat16 CUDA matrix (consecutive columns, any row stride).
+    """Quantise a float32 or bfloat16 CUDA matrix (consecutive columns, rows that do not overlap at any
+    distance; faster where all of them begin at multiples of 32 bytes).
 
     forms: "rows" gives the matrix, in blocks of 32 of a row; "columns" its transpose, in blocks of
     32 of a column; "both" the pair (matrix, transpose) from one pass over x. rounding: "nearest", or
@@ -129,8 +130,8 @@ def onebit_mx4_dequantize(q, dtype=None, out=None, stream=None):
 
 def onebit_mx4_matmul(a, b, out=None, dtype=None, accumulate: bool = False, stream=None):
     """a b^T of two ``Mx4`` matrices of as many columns, float32 sums; bfloat16 (the default) or
-    float32, allocated unless given (consecutive columns, any row stride). accumulate: added to a
-    float32 out."""
+    float32, allocated unless given (consecutive columns, rows that do not overlap at any distance; faster
+    where all of them begin at multiples of 16 bytes). accumulate: added to a float32 out."""
     return _binding().mx4_matmul(_parts(a, "a"), _parts(b, "b"), out, dtype, accumulate, stream)
 
 

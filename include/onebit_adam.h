@@ -705,8 +705,10 @@ int onebit_grad_norm(int32_t ntensors, const int64_t* numel, const void* const* 
  *   key = mix(mix(lo(seed) + G) ^ hi(seed)) ;  w = mix(lo(i/8) + key + hi(i/8) * G)
  *   x = w + ((i%8)/2 + 1) * G ;  x ^= x>>15, x *= 0x8A8866C7, x ^= x>>16
  *   u = i even: x>>16, odd: x & 0xffff
- * Rows of a plain matrix are ld elements apart (ignored for one row); elements are aligned to
- * themselves (eight of them, and ld a multiple of eight, are faster).
+ * Rows of a plain matrix are ld elements apart, its columns at least (ignored for one row). Elements are
+ * aligned to themselves. Faster: quantising (and onebit_mx4_linear) where x, the residual and all of
+ * their rows begin at multiples of 32 bytes, by up to twice; products where out and its rows begin at
+ * multiples of 16, by more than twice where writing them bounds it.
  *
  * Refused (ONEBIT_ERR_ARG, ONEBIT_ERR_ALIGN; the reason in onebit_last_error): what the above
  * excludes, and buffers that are written and overlap another of the call (a plain matrix from its
