@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(kMxThreads) k_mx4_rows8(const Mx4QuantArgs a) 
 // shared memory: for the transposed matrix a thread takes blocks of 32 rows, and its codes go out
 // through shared memory as well, so that 64 bytes of a row are written together. VEC: rows' blocks are
 // aligned to 32 bytes; they are loaded by 32 bytes and more a lane, and the matrix itself is made from
-// registers. Else the values are loaded one by one, consecutive lanes consecutive values.
+// registers. Else the values are loaded one by one, consecutive lanes consecutive values: many loads one
+// after another (8192 x 1000 bf16, rows of 2000 bytes: the matrix 8.1 us, both forms 10.5; of 1024
+// columns 3.6 and 7.6).
 //
 // Shared memory holds a row as pieces of 16 bytes, which are swapped so that the eight lanes of a store
 // (bf16: two rows by four blocks; fp32: a row by eight quarters of blocks) put them into different

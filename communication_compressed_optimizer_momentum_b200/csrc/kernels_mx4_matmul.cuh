@@ -26,9 +26,10 @@ namespace onebit {
 // holds all of them). The tensor cores' own copies (tcgen05.cp) wait for the products before them and
 // hold up those behind: 75 clocks an atom, six for every four products.
 //
-// 8192 x 8192 x 8192 to bf16 takes 164 us, 177 in a row: the tensor pipe is busy 85% of it, at the clock
-// that the power cap leaves (1.55 GHz). Short common axes are bound by loads and results sharing the
-// path to L2 (8192 x 6400 from 1600 columns: 41 us, 30 without storing), small products by their launch.
+// 8192 x 8192 x 8192 to bf16 takes 164 us alone, 174 to 177 as one of 20 in a row, 206 after seconds of
+// them: the tensor pipe is busy 85% of the first, at the clock that the power cap leaves (1.55 GHz). Short
+// common axes are bound by loads and results sharing the path to L2 (8192 x 6400 from 1600 columns: 40 us,
+// up to 55 in programs whose memory lies otherwise; 30 without storing), small products by their launch.
 
 constexpr int kMmThreads = 448;
 constexpr int kOutWarps = 8;              // write out
@@ -354,7 +355,8 @@ __device__ __forceinline__ void take_chunk(uint32_t addr, float* v) {
 // Write a chunk out: rows row .. row + N - 1 of out, of which `rows` (or more) are there. The values
 // go through shared memory and by TMA, which wants aligned rows; else element by element. (bf16 from
 // 1600 columns, 8192 x 6400: two bytes a lane by plain stores 145 us; lanes exchanging values until
-// each has eight columns of a row 61; by TMA 41.)
+// each has eight columns of a row 61; by TMA 41. Rows that TMA does not take still go by two bytes a lane,
+// out of shared memory: 8192 x 6401 92 us.)
 template <int N, typename OT>
 __device__ __forceinline__ void put_chunk(const Mx4MatmulArgs& p, OutWarp& w, float* v, int row,
                                           int rows) {
@@ -746,9 +748,9 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
 // ------------------------------------------------------------------------------------------
 // few rows of a (tokens): no tensor cores
 //
-// A kernel of tensor-core tiles takes longer to set up and join than to read a small b (one token,
-// 4096 x 1024: 4.3 us, here 2.8; 6400 x 1600: 5.0 and 4.5, four tokens 5.8; 8192 x 8192: 8.8 and 11.5,
-// which instructions bound: 2 a weight to make bytes of codes). Twice a code's value is a whole
+// A kernel of tensor-core tiles takes longer to set up and join than to read a small b (4096 x 1024: 3.4
+// us, here one row 2.5, four 3.0; 6400 x 1600: 4.1, here one row 3.8, two 4.1, four 4.7; 8192 x 8192: 8.0,
+// here 10.7, which instructions bound: 2 a weight to make bytes of codes). Twice a code's value is a whole
 // number of at most 12: a block's 32 products are exact in integers (dp4a), and only their sum is
 // scaled, in fp32. x: a in 4 bits, or plain, quantised here as onebit_mx4_quantize does (to nearest).
 //

@@ -322,9 +322,10 @@ int mx4_clear(void* out, int64_t m, int64_t n, int64_t ld, int64_t w, cudaStream
     return ONEBIT_OK;
 }
 
-// Whether few rows are multiplied without the tensor cores: where b is small (see k_mx4_few), and a
-// little longer where that saves a launch that quantises them (one token, 6400 x 1600: 4.9 us, against
-// 2.1 and 5.0).
+// Whether few rows are multiplied without the tensor cores: up to 6M weights, between those where one to
+// four rows gain (4M) and those where four rows lose (10M, 4.7 us against 4.1, and one gains 0.3; see
+// k_mx4_few), and up to 12M where that saves a launch that quantises them (6400 x 1600: one row 4.1 us
+// against 5.4 in two launches, four 5.4 against 5.6).
 bool mx4_few(int64_t m, int64_t n, int64_t k, bool plain) {
     return m <= kFewRows && n * k <= (plain ? (int64_t)3 << 22 : (int64_t)3 << 21);
 }
