@@ -51,7 +51,8 @@ int mx4_plain(const char* where, const char* what, int64_t rows, int64_t cols, c
     if (x == nullptr) return bad(where, std::string("null ") + what);
     if (!aligned_to(x, w))
         return bad(where, std::string(what) + " not aligned to its elements", ONEBIT_ERR_ALIGN);
-    if (rows > 1 && (ld < cols || ld > ((int64_t)1 << 40)))
+    // (a matrix whose places pass 2^60 has no memory, and 64 bits would not count its bytes)
+    if (rows > 1 && (ld < cols || ld > ((int64_t)1 << 40) || ld > ((int64_t)1 << 60) / rows))
         return bad(where, std::string("bad row stride of ") + what);
     return ONEBIT_OK;
 }

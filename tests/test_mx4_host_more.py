@@ -51,3 +51,20 @@ def test_seeds_two_apart_share_no_bits():
     assert len({b.tobytes() for b in bits}) == 2 * len(seeds)
     for i, a in enumerate(bits):                       # equal by chance only: 1 in 65536
         assert all((a == b).sum() < 8 for b in bits[:i])
+
+
+def test_matrices_whose_bytes_64_bits_do_not_count():
+    """Refused before their ranges are compared: (rows - 1) * ld * 4 would come out as anything."""
+    from communication_compressed_optimizer_momentum_b200 import _abi, build
+    build.build()
+    lib = _abi.lib()
+    x, codes, scales = 1 << 40, 1 << 50, 1 << 52
+    for rows, ld in ((1 << 30, 1 << 40), (1 << 25, 1 << 40), ((1 << 20) + 1, 1 << 40)):
+        for rc in (lib.onebit_mx4_quantize(rows, 70, x, 0, ld, codes, scales, None, None, 0, 1, None, 0, None),
+                   lib.onebit_mx4_quantize(rows, 70, x, 1, 70, codes, scales, None, None, 0, 1, 1 << 55, ld,
+                                           None),
+                   lib.onebit_mx4_dequantize(rows, 70, codes, scales, x, 1, ld, None),
+                   lib.onebit_mx4_matmul(rows, 70, 64, codes, scales, 1 << 54, 1 << 55, x, 0, ld, 0, None),
+                   lib.onebit_mx4_linear(rows, 70, 64, x, 0, ld, 1 << 54, 1 << 55, codes, scales, None, None,
+                                         1 << 56, 0, 70, None)):
+            assert rc == -1 and "row stride" in lib.onebit_last_error().decode()
