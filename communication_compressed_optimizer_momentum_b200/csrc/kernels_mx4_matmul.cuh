@@ -19,7 +19,8 @@ namespace onebit {
 //
 // PAIR: two thread blocks of a cluster share a tile of 256 columns by 256 rows of out: each loads its
 // 128 rows of b and half of the rows of a, and one instruction of the first block multiplies in both.
-// That halves what each reads of a.
+// That halves what each reads of a. The codes of both count on one barrier of the first block, which the
+// warp that issues the products waits on; the exponents count in each block, whose warps store them.
 //
 // Warps: 0 loads (TMA), 1 issues the products, 2 to 9 write out (two for each quarter of the lanes), 10
 // to 13 move the exponents from shared to tensor memory (each its quarter of the lanes; every quarter
@@ -28,8 +29,8 @@ namespace onebit {
 //
 // 8192 x 8192 x 8192 to bf16 takes 164 us alone, 174 to 177 as one of 20 in a row, 206 after seconds of
 // them: the tensor pipe is busy 85% of the first, at the clock that the power cap leaves (1.55 GHz). Short
-// common axes are bound by loads and results sharing the path to L2 (8192 x 6400 from 1600 columns: 40 us,
-// up to 55 in programs whose memory lies otherwise; 30 without storing), small products by their launch.
+// common axes are bound by loads and results sharing the path to L2 (8192 x 6400 from 1600 columns: 41 us,
+// up to 45 in programs whose memory lies otherwise; 30 without storing), small products by their launch.
 
 constexpr int kMmThreads = 448;
 constexpr int kOutWarps = 8;              // write out
@@ -135,6 +136,16 @@ __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int 
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The same for a pair, counted on a barrier of either block (`bar`: its address for the cluster).
+__device__ __forceinline__ void tma_tile_pair(void* dst, const CUtensorMap* map, int x, int y,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
@@ -279,12 +290,8 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
 // - Tensor memory (the exponents that are stored, the accumulators that are read) is ordered by the
 //   tensor cores' own fences: the operation and its wait, tcgen05.fence::before_thread_sync, a relaxed
 //   arrival; a relaxed wait, tcgen05.fence::after_thread_sync, the product. PTX gives this pattern.
-// - The second block's codes are copied by TMA, seen to be complete by the second block's warps (an
-//   acquire on the barrier that counts their bytes) before they arrive, and read by the tensor cores of
-//   the SM whose shared memory holds them. PTX's memory model has no rule that carries the first block's
-//   product behind this chain, which holds an arrival without release: it rests on shared memory being
-//   in one place. A copy counts its bytes where it has written them, nothing keeps other copies of them,
-//   and the product is issued after the arrival. (Products repeat bit for bit; tests compare them in full.)
+// - The codes that the second block copies count on a barrier of the first, where the thread that issues
+//   the products waits for them itself.
 template <bool PAIR>
 __device__ __forceinline__ void pair_arrive(uint64_t* bar) {
     if constexpr (PAIR)
@@ -436,7 +443,8 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
     uint64_t* const full = reinterpret_cast<uint64_t*>(sm + S::kStages * S::kStage + S::kParts);
     uint64_t* const ready = full + S::kStages;      // ... and the exponents are in tensor memory
     uint64_t* const empty = ready + S::kStages;
-    uint64_t* const done = empty + S::kStages;      // [2] an accumulator is complete
+    uint64_t* const codes = empty + S::kStages;     // PAIR: both blocks' codes, in the first one's
+    uint64_t* const done = codes + S::kStages;      // [2] an accumulator is complete
     uint64_t* const drained = done + 2;             // [2] ... and read as far as the next needs
     uint64_t* const last = drained + 2;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(last + 1);
@@ -447,6 +455,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             mbar_init(full + i, 1);
             mbar_init(ready + i, 4 * S::kGroup);
             mbar_init(empty + i, 1);
+            mbar_init(codes + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(done + i, 1);
@@ -514,9 +523,21 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                 if (!(ok = warp_wait(empty + stage, phase ^ 1, p.wait_ns))) break;
                 uint8_t* s = sm + stage * S::kStage;
                 if (elect()) {
-                    mbar_arrive_expect_tx(full + stage, S::kStage);
-                    tma_tile(s, &maps.b, k * 128, brow * kMmLanes, full + stage);
-                    tma_tile(s + S::kB, &maps.a, k * 128, tm * TM + bank * S::kARows, full + stage);
+                    // A pair's codes count where they are waited for. (The second block's may come
+                    // before the first has said how many bytes to expect, but not in another phase: that
+                    // stage's last products have waited for all of the last phase.)
+                    const int arow0 = tm * TM + bank * S::kARows;
+                    if constexpr (PAIR) {
+                        const uint32_t bar = cluster_addr(smem_addr(codes + stage), 0);
+                        if (bank == 0) mbar_arrive_expect_tx(codes + stage, 2 * (S::kB + S::kA));
+                        tma_tile_pair(s, &maps.b, k * 128, brow * kMmLanes, bar);
+                        tma_tile_pair(s + S::kB, &maps.a, k * 128, arow0, bar);
+                        mbar_arrive_expect_tx(full + stage, S::kSB + S::kSA);
+                    } else {
+                        mbar_arrive_expect_tx(full + stage, S::kStage);
+                        tma_tile(s, &maps.b, k * 128, brow * kMmLanes, full + stage);
+                        tma_tile(s + S::kB, &maps.a, k * 128, arow0, full + stage);
+                    }
                     tma_tile(s + S::kB + S::kA, &maps.sb, k * 256, brow, full + stage);
                     tma_tile(s + S::kB + S::kA + S::kSB, &maps.sa, k * 256, arow, full + stage);
                 }
@@ -529,8 +550,14 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             }
         }
         if (lane == 0) {         // leave no copy in flight behind
-            for (int64_t f = filled > S::kStages ? filled - S::kStages : 0; f < filled; ++f)
-                ok = mm_wait(full + f % S::kStages, (uint32_t)(f / S::kStages) & 1, kMmWaitNs) && ok;
+            for (int64_t f = filled > S::kStages ? filled - S::kStages : 0; f < filled; ++f) {
+                const int at = (int)(f % S::kStages);
+                const uint32_t parity = (uint32_t)(f / S::kStages) & 1;
+                ok = mm_wait(full + at, parity, kMmWaitNs) && ok;
+                // A pair's codes: the products that read them are done, or a wait of this warp has run
+                // out since they were queued (a copy takes microseconds, a wait a millisecond at least).
+                if (PAIR && ok) ok = mm_wait(empty + at, parity, p.wait_ns);
+            }
             // ... nor an arrival from a pair's other block, which may wait as long for one thing more
             if (PAIR && bank == 1) ok = mm_wait(last, 0, 4 * kMmWaitNs) && ok;
             if (!ok) atomicOr(&g_mx4_status, kMmTimeout);
@@ -551,6 +578,7 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++c) {
                 if (!(ok = warp_wait<PAIR>(ready + stage, phase, p.wait_ns))) break;
+                if (PAIR && !(ok = warp_wait(codes + stage, phase, p.wait_ns))) break;
                 tc_fence_after();
                 const uint32_t s = smem_addr(sm + stage * S::kStage);
                 const uint32_t eb = tmem + S::kExp + (c % S::kExpBuffers) * S::kExpCols, ea = eb + 8;
