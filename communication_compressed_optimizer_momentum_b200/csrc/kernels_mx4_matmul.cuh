@@ -27,10 +27,10 @@ namespace onebit {
 // holds all of them). The tensor cores' own copies (tcgen05.cp) wait for the products before them and
 // hold up those behind: 75 clocks an atom, six for every four products.
 //
-// 8192 x 8192 x 8192 to bf16 takes 164 us alone, 174 to 177 as one of 20 in a row, 206 after seconds of
-// them: the tensor pipe is busy 85% of the first, at the clock that the power cap leaves (1.55 GHz). Short
+// 8192 x 8192 x 8192 to bf16 takes 166 us alone, 176 to 183 as one of 20 in a row, 210 after seconds of
+// them: the tensor pipe is busy 85% of the time, at the clock that the power cap leaves (1.52 GHz). Short
 // common axes are bound by loads and results sharing the path to L2 (8192 x 6400 from 1600 columns: 41 us,
-// up to 45 in programs whose memory lies otherwise; 30 without storing), small products by their launch.
+// up to 54 in programs whose memory lies otherwise; 30 without storing), small products by their launch.
 
 constexpr int kMmThreads = 448;
 constexpr int kOutWarps = 8;              // write out
@@ -58,18 +58,20 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 
 // Wait for phase `parity` of the barrier, giving up after `limit` ns (a long common axis keeps the warps
 // that write out waiting for a good while: a number of polls would not say how long; 256 polls take 1 ms
-// where nothing comes).
+// where nothing comes). The loops stay loops: unrolled, a layer's three passes take 1 us more.
 // PAIR: arrivals come from the other block too (pair_arrive).
 template <bool PAIR = false>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
     const auto there = [&] {
         return PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
     };
+#pragma unroll 1
     for (int i = 0; i < 256; ++i)
         if (there()) return true;
     uint64_t start, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
     do {
+#pragma unroll 1
         for (int i = 0; i < 256; ++i)
             if (there()) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
@@ -577,8 +579,9 @@ k_mx4_matmul(const __grid_constant__ Mx4Maps maps, const Mx4MatmulArgs p) {
                 break;
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++c) {
-                if (!(ok = warp_wait<PAIR>(ready + stage, phase, p.wait_ns))) break;
+                // (the codes come before the exponents are stored: the second wait is the longer one)
                 if (PAIR && !(ok = warp_wait(codes + stage, phase, p.wait_ns))) break;
+                if (!(ok = warp_wait<PAIR>(ready + stage, phase, p.wait_ns))) break;
                 tc_fence_after();
                 const uint32_t s = smem_addr(sm + stage * S::kStage);
                 const uint32_t eb = tmem + S::kExp + (c % S::kExpBuffers) * S::kExpCols, ea = eb + 8;
